@@ -1,0 +1,714 @@
+// Linears with a fused epilogue and their gradients, one tcgen05 GEMM kernel in
+// three operand orders:
+//   forward   y  = residual + act(x w^T + bias)     A = x  [rows, C],  B = w [O, C]
+//   dgrad     dx = (dy w) * act'(x_pre)             A = dy [rows, O],  B = w read along C
+//   wgrad     dw = dy^T x                           A = dy read along O, B = x read along C,
+//                                                   K = the rows
+// "Read along" operands are MN-major for the tensor core: the same row-major
+// tensors in memory, with no transposed copy.
+//
+// Tensors come as 4-D views [B, heads, N, D] (heads = 1: rows), so the products read
+// and write head layouts and strided tensors through the TMA maps and the
+// epilogue's addresses; a 64-column block never crosses a head (D is 64 or 128).
+//
+// Design as in the head projection: one persistent CTA per SM over 256 x 256 output
+// tiles; warp 0 loads 64-wide K blocks of both operands (32 + 32 KB, 128-byte
+// swizzle) into a 3-stage ring by TMA, one lane of warp 1 issues M = 128, N = 256
+// tcgen05.mma into a 2 x 256-column TMEM accumulator (all of it), warps 2-9 take the
+// accumulator out, a row per thread.  Column tiles go in groups whose B rows take at
+// most 32 MB.  Every wait is bounded (abort flag and status word).
+#include <algorithm>
+
+#include "block_internal.h"
+#include "sm100.cuh"
+
+namespace vsa {
+namespace {
+using namespace sm100;
+
+constexpr int kBM = 256, kBN = 256, kBK = 64, kStages = 3;
+constexpr int kThreads = 320;                     // TMA, MMA, 8 epilogue warps
+constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kHalfA = 128 * kBK * 2;             // rows 128-255 of the tile, in both orders
+constexpr int kMnAtom = 64 * kBK * 2;             // one 64-column x 64-row box
+constexpr int kNBar = 2 * kStages + 3;            // full[S], empty[S], acc_full, acc_empty, drain
+// stages, barriers, TMEM slot and abort flag, then each epilogue warp's copy of the tile's biases
+constexpr size_t kSmem = size_t(kStages) * kStageBytes + kNBar * 8 + 16 + 8 * kBN * 4 + 1024;
+
+enum Order { kForward = 0, kDgrad = 1, kWgrad = 2 };
+
+// Column c of a view -> (head, channel).
+struct Cols {
+  int D;          // channels of a head (all of them for rows)
+  int blocks;     // 64-wide blocks of a head
+};
+
+struct OutView {
+  uint16_t* ptr;
+  int64_t sb, sh, sn;
+  int D;
+};
+
+struct GemmArgs {
+  unsigned int* status;
+  int m_tiles, n_tiles, group;     // output tiles and the column group of the order
+  int k_blocks, k_split, splits;   // K blocks, and how many one split takes
+  int rows_b;                      // row blocks (tiles, or K blocks in wgrad) per batch element
+  int64_t N;                       // rows of a batch element of the TMA views
+  int64_t M;                       // valid rows of the output (rows of dw in wgrad)
+  int cols;                        // valid columns of the output
+  Cols ac, bc;                     // columns of A and B along the contiguous dimension
+  // epilogue
+  int64_t Nrow;                    // rows per batch element of the output views
+  OutView y, res, pre;
+  const void* bias;
+  int bias_f32, act;
+  float* partial;                  // wgrad with splits > 1: fp32 [splits][M][cols]
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ void decode(int t, const GemmArgs& a, int& m, int& n) {
+  const int G = a.group;
+  const int g = t / (a.m_tiles * G), r = t % (a.m_tiles * G);
+  const int gw = min(G, a.n_tiles - g * G);
+  m = r / gw;
+  n = g * G + r % gw;
+}
+
+// exp(-x) overflows to infinity for x < -88, where 1 / (1 + inf) = 0 is the limit.
+__device__ __forceinline__ float sigmoid_f(float x) {
+  return __fdividef(1.0f, 1.0f + __expf(-x));
+}
+constexpr float kGeluC = 1.5957691216057308f;     // 2 sqrt(2/pi)
+__device__ __forceinline__ float gelu_arg(float x) { return kGeluC * fmaf(0.044715f * x * x, x, x); }
+
+// f = act(f) for a run of values; the choice is uniform and taken once a run.
+template <int kN>
+__device__ __forceinline__ void act_run(int act, float (&f)[kN]) {
+  if (act == VSA_ACT_GELU_TANH) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) f[e] *= sigmoid_f(gelu_arg(f[e]));
+  } else if (act == VSA_ACT_SILU) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) f[e] *= sigmoid_f(f[e]);
+  } else if (act == VSA_ACT_SIGMOID) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) f[e] = sigmoid_f(f[e]);
+  }
+}
+
+// f *= act'(x).
+template <int kN>
+__device__ __forceinline__ void slope_run(int act, const float (&x)[kN], float (&f)[kN]) {
+  if (act == VSA_ACT_GELU_TANH) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      // s is 0 in fp32 for x < -10 and 1 - s for x > 6, so the clamp only keeps an overflow
+      // of the square from meeting that 0
+      const float s = sigmoid_f(gelu_arg(x[e])), c = fminf(fmaxf(x[e], -20.0f), 20.0f);
+      f[e] *= fmaf(c * s * (1.0f - s), kGeluC * fmaf(0.134145f * c, c, 1.0f), s);
+    }
+  } else if (act == VSA_ACT_SILU) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      const float s = sigmoid_f(x[e]);
+      f[e] *= fmaf(x[e] * s, 1.0f - s, s);
+    }
+  } else if (act == VSA_ACT_SIGMOID) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      const float s = sigmoid_f(x[e]);
+      f[e] *= s * (1.0f - s);
+    }
+  }
+}
+
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = __uint_as_float(w[e] << 16);
+    f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                    pack_bf16(f[6], f[7]));
+}
+
+// 64 columns from col of a view's row (column blocks of 64 lie within a head).
+__device__ __forceinline__ uint16_t* out_row(const OutView& v, int64_t b, int64_t n, int col) {
+  const int h = col / v.D;
+  return v.ptr + b * v.sb + h * v.sh + n * v.sn + (col - h * v.D);
+}
+
+template <int kOrder>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                  const __grid_constant__ GemmArgs a) {
+  constexpr bool kAMn = kOrder == kWgrad, kBMn = kOrder != kForward;
+  constexpr uint32_t kIdesc = idesc_bf16(128, kBN, kAMn, kBMn);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t s_base = smem_u32(smem);
+  const uint32_t bar0 = s_base + kStages * kStageBytes;
+  const uint32_t full = bar0, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
+                 acc_empty = acc_full + 8, drain = acc_empty + 8;
+  uint8_t* tail = smem + kStages * kStageBytes + kNBar * 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
+  float* s_bias = reinterpret_cast<float*>(tail + 16 - (kNBar * 8) % 16);   // 16-byte aligned
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = a.m_tiles * a.n_tiles * a.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 256);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA
+    if (lane == 0) {
+      uint32_t g = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        int m, n;
+        const int sp = t % a.splits;
+        decode(t / a.splits, a, m, n);
+        const int k0 = sp * a.k_split, k1 = min(a.k_blocks, k0 + a.k_split);
+        for (int kb = k0; kb < k1; ++kb, ++g) {
+          const uint32_t s = g % kStages;
+          if (g >= uint32_t(kStages) &&
+              !wait_bar(empty + 8 * s, ((g / kStages) - 1) & 1, abort_flag, a.status, 31)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = s_base + s * kStageBytes, sb = sa + kABytes, bar = full + 8 * s;
+          mbar_expect_tx(bar, kStageBytes);
+          if (!kAMn) {
+            // row tile m, K block kb of A's columns
+            const int h = kb / a.ac.blocks, d0 = (kb % a.ac.blocks) * kBK;
+            tma_load_4d(sa, &tm_a, bar, d0, (m % a.rows_b) * kBM, h, m / a.rows_b);
+            const int k = h * a.ac.D + d0;
+            if (!kBMn) {
+              tma_load_4d(sb, &tm_b, bar, k, n * kBN, 0, 0);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kBN / 64; ++i)
+                tma_load_4d(sb + i * kMnAtom, &tm_b, bar, n * kBN + 64 * i, k, 0, 0);
+            }
+          } else {
+            const int b = kb / a.rows_b, r0 = (kb % a.rows_b) * kBK;
+#pragma unroll
+            for (int i = 0; i < kBM / 64; ++i) {
+              const int c = m * kBM + 64 * i, h = c / a.ac.D;
+              tma_load_4d(sa + i * kMnAtom, &tm_a, bar, c - h * a.ac.D, r0, h, b);
+            }
+#pragma unroll
+            for (int i = 0; i < kBN / 64; ++i) {
+              const int c = n * kBN + 64 * i, h = c / a.bc.D;
+              tma_load_4d(sb + i * kMnAtom, &tm_b, bar, c - h * a.bc.D, r0, h, b);
+            }
+          }
+        }
+      }
+      if (!ok) {
+        // abort: none of our TMA writes may still be in flight
+        for (uint32_t x = (g > uint32_t(kStages) ? g - kStages : 0); x < g; ++x)
+          wait_bar_drain(full + 8 * (x % kStages), (x / kStages) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0) {
+      uint32_t g = 0;
+      int lt = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++lt) {
+        const int k0 = (t % a.splits) * a.k_split;
+        const int nk = min(a.k_blocks, k0 + a.k_split) - k0;
+        if (lt >= 1 && !wait_bar(acc_empty, (lt - 1) & 1, abort_flag, a.status, 32)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kb = 0; kb < nk && ok; ++kb, ++g) {
+          const uint32_t s = g % kStages;
+          if (!wait_bar(full + 8 * s, (g / kStages) & 1, abort_flag, a.status, 33)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = s_base + s * kStageBytes, sb = sa + kABytes;
+#pragma unroll
+          for (int ks = 0; ks < kBK / 16; ++ks) {
+            // K-major: 16 columns on; MN-major: 16 rows of 128 bytes on, 64-column atoms
+            // kMnAtom apart
+            const uint64_t bd = kBMn ? sdesc_sw128(sb + ks * 2048, kMnAtom, 1024)
+                                     : sdesc_sw128(sb + ks * 32, 16, 1024);
+            const uint32_t ka = sa + ks * (kAMn ? 2048 : 32);
+            const uint64_t a0 = kAMn ? sdesc_sw128(ka, kMnAtom, 1024) : sdesc_sw128(ka, 16, 1024);
+            const uint64_t a1 = kAMn ? sdesc_sw128(ka + kHalfA, kMnAtom, 1024)
+                                     : sdesc_sw128(ka + kHalfA, 16, 1024);
+            const uint32_t accum = (kb > 0 || ks > 0) ? 1u : 0u;
+            umma_bf16(tmem, a0, bd, kIdesc, accum);
+            umma_bf16(tmem + kBN, a1, bd, kIdesc, accum);
+          }
+          umma_commit(empty + 8 * s);
+        }
+        if (ok) umma_commit(acc_full);
+      }
+      // drain: every MMA issued above complete before TMEM is freed
+      umma_commit(drain);
+      wait_bar_drain(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int quad = warp & 3;                       // TMEM lane quadrant of this warp
+    const int half = (warp - 2) >> 2;                // rows 0-127 or 128-255 of the tile
+    const int row = half * 128 + quad * 32 + lane;
+    const uint32_t t_row = tmem + (uint32_t(quad * 32) << 16) + uint32_t(half * kBN);
+    float* bias = s_bias + (warp - 2) * kBN;
+    int lt = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++lt) {
+      int m, n;
+      const int sp = t % a.splits;
+      decode(t / a.splits, a, m, n);
+      // this thread's row of the output, as (batch element, row)
+      int64_t r, b, tok;
+      bool live;
+      if (kOrder == kWgrad) {
+        r = int64_t(m) * kBM + row;
+        live = r < a.M;
+        b = 0;
+        tok = r;
+      } else {
+        const int64_t in_b = int64_t(m % a.rows_b) * kBM + row;
+        r = int64_t(m / a.rows_b) * a.N + in_b;
+        live = in_b < a.N;
+        b = r / a.Nrow;
+        tok = r - b * a.Nrow;
+      }
+      if (kOrder == kForward && a.bias != nullptr) {
+        // the tile's 256 biases, each warp its own copy: no barrier among warps, one of
+        // which may leave the loop on an abort
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kBN / 32; ++i) {
+          const int col = n * kBN + 32 * i + lane;
+          float v = 0.0f;
+          if (col < a.cols)
+            v = a.bias_f32
+                    ? __ldg(static_cast<const float*>(a.bias) + col)
+                    : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.bias) + col)) << 16);
+          bias[32 * i + lane] = v;
+        }
+        __syncwarp();
+      }
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(acc_full, lt & 1, abort_flag, a.status, 34))) break;
+      tc_fence_after();
+      if (kOrder == kWgrad && a.splits > 1) {
+        float* dst = a.partial + (int64_t(sp) * a.M + r) * a.cols;
+#pragma unroll 1
+        for (int c = 0; c < kBN / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(t_row + 32 * c, v);
+          tmem_wait_ld(v);
+          const int col0 = n * kBN + 32 * c;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (live && col0 + 4 * q < a.cols)
+              *reinterpret_cast<uint4*>(dst + col0 + 4 * q) =
+                  make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+        tc_fence_before();
+        mbar_arrive(acc_empty);
+        continue;
+      }
+#pragma unroll 1
+      for (int c = 0; c < kBN / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(t_row + 32 * c, v);
+        tmem_wait_ld(v);
+        if (c == kBN / 32 - 1) {
+          tc_fence_before();
+          mbar_arrive(acc_empty);                      // the MMAs of the next tile may start
+        }
+        const int col0 = n * kBN + 32 * c;
+        if (!live || col0 >= a.cols) continue;
+        if (kOrder == kForward && a.bias != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            v[e] = __float_as_uint(__uint_as_float(v[e]) + bias[32 * c + e]);
+        }
+        uint16_t* yp = out_row(a.y, b, tok, col0);
+        const uint16_t* rp = nullptr;
+        uint16_t* pp = nullptr;
+        if (kOrder != kWgrad && a.res.ptr != nullptr) rp = out_row(a.res, b, tok, col0);
+        if (kOrder == kForward && a.pre.ptr != nullptr) pp = out_row(a.pre, b, tok, col0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (col0 + 8 * q >= a.cols) break;
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q + e]);
+          uint4 rr = make_uint4(0u, 0u, 0u, 0u);
+          if (rp != nullptr) rr = *reinterpret_cast<const uint4*>(rp + 8 * q);
+          float x[8];
+          unpack(rr, x);
+          if (kOrder == kForward) {
+            if (pp != nullptr) *reinterpret_cast<uint4*>(pp + 8 * q) = pack(f);
+            act_run(a.act, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] += x[e];
+          } else if (kOrder == kDgrad && rp != nullptr) {
+            slope_run(a.act, x, f);
+          }
+          *reinterpret_cast<uint4*>(yp + 8 * q) = pack(f);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+  }
+}
+
+// dw = bf16(sum over splits of the fp32 partial products), in split order.
+__global__ void __launch_bounds__(256) split_sum_kernel(const float4* __restrict__ partial,
+                                                        uint2* __restrict__ out, int64_t n4,
+                                                        int splits) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n4; i += int64_t(gridDim.x) * 256) {
+    float4 s = partial[i];
+    for (int k = 1; k < splits; ++k) {
+      const float4 v = partial[int64_t(k) * n4 + i];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    out[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+  }
+}
+
+// Column sums of dy [B, heads, N, D] -> fp32 [O]: a block takes 256 columns (32 lanes of 8) of a
+// run of rows, 8 warps side by side; part[blockIdx.y][O], summed by colsum_join_kernel.
+__global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, int64_t Nrow, int64_t M,
+                                                     int O, int64_t rows_per, float* part) {
+  __shared__ float s[8][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 256 + 8 * lane;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const int64_t r0 = int64_t(blockIdx.y) * rows_per, r1 = min(M, r0 + rows_per);
+  if (col < O) {
+#pragma unroll 4
+    for (int64_t r = r0 + warp; r < r1; r += 8) {
+      const int64_t b = r / Nrow;
+      const uint4 v = *reinterpret_cast<const uint4*>(out_row(dy, b, r - b * Nrow, col));
+      float f[8];
+      unpack(v, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += f[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[warp][8 * lane + e] = acc[e];
+  __syncthreads();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c < O) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += s[w][threadIdx.x];
+    part[int64_t(blockIdx.y) * O + c] = v;
+  }
+}
+
+__global__ void __launch_bounds__(256) colsum_join_kernel(const float* part, int runs, int O,
+                                                          float* db) {
+  __shared__ float s[8][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < O)
+    for (int i = warp; i < runs; i += 8) v += part[int64_t(i) * O + c];
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < O) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += s[w][lane];
+    db[c] = t;
+  }
+}
+
+__global__ void __launch_bounds__(256) act_backward_kernel(const uint4* dy, const uint4* pre, int act,
+                                                           uint4* out, int64_t n8) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n8; i += int64_t(gridDim.x) * 256) {
+    float g[8], x[8];
+    unpack(dy[i], g);
+    unpack(pre[i], x);
+    slope_run(act, x, g);
+    out[i] = pack(g);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+// A view as the products see it: heads >= 1, rows as one batch element when they are
+// evenly spaced over all of them.
+struct View {
+  const uint16_t* ptr;
+  int64_t sb, sh, sn, B, N;
+  int H, D;
+};
+
+View make_view(const vsa_view& v, int B, int64_t N, int heads, int C) {
+  View o = {static_cast<const uint16_t*>(v.ptr), v.stride_b, v.stride_h, v.stride_n, B, N, 1, C};
+  if (heads > 0) {
+    o.H = heads;
+    o.D = C / heads;
+  }
+  return o;
+}
+
+bool rows_even(const View& v) { return v.B == 1 || v.N == 1 || v.sb == v.N * v.sn; }
+
+void flatten(View* v) {
+  if (v->N == 1 && v->B > 1) v->sn = v->sb;
+  v->N *= v->B;
+  v->B = 1;
+}
+
+// TMA map of a view, box 64 channels x box_rows rows, 128-byte swizzle.
+bool map_view(CUtensorMap* m, const View& v, int box_rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[4] = {cuuint64_t(v.D), cuuint64_t(v.N), cuuint64_t(v.H), cuuint64_t(v.B)};
+  // the stride of a dimension of extent 1 is not used, but has to be valid
+  const auto bytes = [](int64_t extent, int64_t stride) {
+    return extent > 1 ? cuuint64_t(stride) * 2 : cuuint64_t(16);
+  };
+  const cuuint64_t strides[3] = {bytes(v.N, v.sn), bytes(v.H, v.sh), bytes(v.B, v.sb)};
+  const cuuint32_t box[4] = {64u, cuuint32_t(box_rows), 1u, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(v.ptr), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+View matrix(const void* p, int64_t rows, int cols) {
+  return View{static_cast<const uint16_t*>(p), 0, 0, cols, 1, rows, 1, cols};
+}
+
+OutView out_view(const vsa_view& v, int heads, int C) {
+  return OutView{static_cast<uint16_t*>(v.ptr), v.stride_b, heads > 0 ? v.stride_h : 0, v.stride_n,
+                 heads > 0 ? C / heads : C};
+}
+
+Cols cols_of(const View& v) { return Cols{v.D, (v.D + kBK - 1) / kBK}; }
+
+int sms(const vsa_plan_s* p) { return p->num_sms > 0 ? p->num_sms : 148; }
+
+// Splits of the rows of a weight gradient: as many as leave every SM a tile of at least
+// 8 K blocks.
+int wgrad_splits(const vsa_plan_s* p, int O, int C, int k_blocks) {
+  const int64_t tiles = int64_t((O + kBM - 1) / kBM) * ((C + kBN - 1) / kBN);
+  return int(std::max<int64_t>(1, std::min<int64_t>(sms(p) / tiles, k_blocks / 8)));
+}
+
+int row_blocks(const View& v, int rows) { return int((v.N + rows - 1) / rows); }
+
+constexpr int64_t kColsumRows = 256;      // rows of a column-sum block, at least
+
+int colsum_runs(int64_t M) {
+  return int(std::max<int64_t>(1, std::min<int64_t>(256, (M + kColsumRows - 1) / kColsumRows)));
+}
+
+template <int kOrder>
+vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv, int b_box,
+                  GemmArgs a, int64_t b_bytes, cudaStream_t stream) {
+  CUtensorMap ma, mb;
+  if (!map_view(&ma, av, a_box) || !map_view(&mb, bv, b_box))
+    return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+  cudaError_t e = cudaFuncSetAttribute(linear_kernel<kOrder>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+  if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
+  const int64_t groups = std::max<int64_t>(1, (b_bytes + (int64_t(32) << 20) - 1) >> 25);
+  a.group = int(std::max<int64_t>(1, (a.n_tiles + groups - 1) / groups));
+  a.status = p->d_status;
+  const int64_t tiles = int64_t(a.m_tiles) * a.n_tiles * a.splits;
+  if (tiles >= (int64_t(1) << 31)) return fail(VSA_ERR_UNSUPPORTED, "too many output tiles");
+  const int grid = int(std::min<int64_t>(tiles, sms(p)));
+  linear_kernel<kOrder><<<grid, kThreads, kSmem, stream>>>(ma, mb, a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? VSA_OK
+                          : fail(VSA_ERR_CUDA, std::string("linear launch: ") + cudaGetErrorString(e));
+}
+
+}  // namespace
+
+vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, cudaStream_t stream) {
+  View x = make_view(q.x, q.B, q.N, q.x_heads, q.C);
+  if (rows_even(x)) flatten(&x);
+  GemmArgs a = {};
+  a.rows_b = row_blocks(x, kBM);
+  a.m_tiles = int(x.B) * a.rows_b;
+  a.n_tiles = (q.O + kBN - 1) / kBN;
+  a.ac = cols_of(x);
+  a.k_blocks = x.H * a.ac.blocks;
+  a.k_split = a.k_blocks;
+  a.splits = 1;
+  a.N = x.N;
+  a.M = x.B * x.N;
+  a.cols = q.O;
+  a.Nrow = q.N;
+  a.y = out_view(q.y, q.y_heads, q.O);
+  a.res = out_view(q.residual, q.y_heads, q.O);
+  a.pre = out_view(q.pre, q.y_heads, q.O);
+  a.bias = q.bias;
+  a.bias_f32 = q.bias_type == VSA_F32;
+  a.act = q.act;
+  return launch<kForward>(p, x, kBM, matrix(q.w, q.O, q.C), kBN, a, int64_t(q.O) * q.C * 2, stream);
+}
+
+size_t linear_backward_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
+  // the K blocks of either flattening
+  const int64_t M = int64_t(B) * N;
+  const int64_t kb = std::max((M + kBK - 1) / kBK, int64_t(B) * ((N + kBK - 1) / kBK));
+  const int s = wgrad_splits(p, O, C, int(std::min<int64_t>(kb, 1 << 30)));
+  const size_t split = s > 1 ? size_t(s) * O * C * sizeof(float) : 0;
+  const size_t sums = size_t(colsum_runs(M)) * O * sizeof(float);
+  return (split + 15) / 16 * 16 + sums;
+}
+
+vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_args& q, void* ws,
+                                  cudaStream_t stream) {
+  const int64_t M = int64_t(q.B) * q.N;
+  if (M == 0) {
+    cudaError_t e = cudaSuccess;
+    if (q.dw != nullptr) e = cudaMemsetAsync(q.dw, 0, size_t(q.O) * q.C * 2, stream);
+    if (e == cudaSuccess && q.db != nullptr) e = cudaMemsetAsync(q.db, 0, size_t(q.O) * 4, stream);
+    return e == cudaSuccess ? VSA_OK : fail(VSA_ERR_CUDA, cudaGetErrorString(e));
+  }
+  const View dy = make_view(q.dy, q.B, q.N, q.y_heads, q.O);
+  if (q.dx.ptr != nullptr) {
+    View g = dy;
+    if (rows_even(g)) flatten(&g);
+    GemmArgs a = {};
+    a.rows_b = row_blocks(g, kBM);
+    a.m_tiles = int(g.B) * a.rows_b;
+    a.n_tiles = (q.C + kBN - 1) / kBN;
+    a.ac = cols_of(g);
+    a.k_blocks = g.H * a.ac.blocks;
+    a.k_split = a.k_blocks;
+    a.splits = 1;
+    a.N = g.N;
+    a.M = M;
+    a.cols = q.C;
+    a.Nrow = q.N;
+    a.y = out_view(q.dx, q.x_heads, q.C);
+    a.res = out_view(q.x_pre, q.x_heads, q.C);
+    a.act = q.x_act;
+    const vsa_status st = launch<kDgrad>(p, g, kBM, matrix(q.w, q.O, q.C), kBK, a,
+                                         int64_t(q.O) * q.C * 2, stream);
+    if (st != VSA_OK) return st;
+  }
+  float* sums = static_cast<float*>(ws);
+  if (q.dw != nullptr) {
+    View g = dy, x = make_view(q.x, q.B, q.N, q.x_heads, q.C);
+    if (rows_even(g) && rows_even(x)) {
+      flatten(&g);
+      flatten(&x);
+    }
+    GemmArgs a = {};
+    a.rows_b = row_blocks(g, kBK);
+    a.k_blocks = int(g.B) * a.rows_b;
+    a.splits = wgrad_splits(p, q.O, q.C, a.k_blocks);
+    a.k_split = (a.k_blocks + a.splits - 1) / a.splits;
+    a.splits = (a.k_blocks + a.k_split - 1) / a.k_split;
+    a.m_tiles = (q.O + kBM - 1) / kBM;
+    a.n_tiles = (q.C + kBN - 1) / kBN;
+    a.ac = cols_of(g);
+    a.bc = cols_of(x);
+    a.N = g.N;
+    a.M = q.O;
+    a.cols = q.C;
+    a.Nrow = q.O;
+    a.y = OutView{static_cast<uint16_t*>(q.dw), 0, 0, q.C, q.C};
+    a.partial = static_cast<float*>(ws);
+    // the rows are long: all column tiles of one group share the pass over them
+    const vsa_status st = launch<kWgrad>(p, g, kBK, x, kBK, a, 0, stream);
+    if (st != VSA_OK) return st;
+    if (a.splits > 1) {
+      const int64_t n4 = int64_t(q.O) * q.C / 4;
+      const int blocks = int(std::min<int64_t>((n4 + 255) / 256, int64_t(sms(p)) * 8));
+      split_sum_kernel<<<blocks, 256, 0, stream>>>(static_cast<const float4*>(ws),
+                                                   static_cast<uint2*>(q.dw), n4, a.splits);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
+      sums += (int64_t(a.splits) * q.O * q.C + 3) / 4 * 4;
+    }
+  }
+  if (q.db != nullptr) {
+    const int runs = colsum_runs(M);
+    const int64_t rows_per = (M + runs - 1) / runs;
+    colsum_kernel<<<dim3((q.O + 255) / 256, runs), 256, 0, stream>>>(
+        out_view(q.dy, q.y_heads, q.O), q.N, M, q.O, rows_per, sums);
+    colsum_join_kernel<<<(q.O + 31) / 32, 256, 0, stream>>>(sums, runs, q.O, q.db);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
+  }
+  return VSA_OK;
+}
+
+cudaError_t launch_act_backward(const void* dy, const void* pre, int act, void* out, int64_t n,
+                                int num_sms, cudaStream_t stream) {
+  const int64_t n8 = n / 8;
+  const int blocks = int(std::min<int64_t>((n8 + 255) / 256, int64_t(num_sms > 0 ? num_sms : 148) * 8));
+  act_backward_kernel<<<blocks, 256, 0, stream>>>(static_cast<const uint4*>(dy),
+                                                  static_cast<const uint4*>(pre), act,
+                                                  static_cast<uint4*>(out), n8);
+  return cudaGetLastError();
+}
+
+}  // namespace vsa

@@ -53,6 +53,10 @@ vsa_status build_plan(const vsa_geometry& g, vsa_plan_s* p) {
   p->n_tokens = N;
   p->n_tiles = int(T);
   p->n_prefix_tiles = int(n_p);
+  p->n_prefix_tokens = P;
+  p->grid[0] = int(Tg);
+  p->grid[1] = int(Hg);
+  p->grid[2] = int(Wg);
   p->n_padded = T * R;
   p->untile.assign(size_t(N), -1);
   p->row_src.assign(size_t(T * R), -1);

@@ -18,6 +18,8 @@ struct vsa_plan_s {
   int64_t n_padded = 0;      // N_pad = T * R
   int n_tiles = 0;           // T
   int n_prefix_tiles = 0;    // n_p
+  int64_t n_prefix_tokens = 0;
+  int grid[3] = {0, 0, 0};   // video grid (time, height, width)
   // host tables
   std::vector<int32_t> untile, row_src, block_len, tile_seg;
   // device side (device < 0: host-only plan)

@@ -4,13 +4,13 @@ Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels.  PyTorch supplies device memory and the current stream.  There is no
 fallback: if ``libvsa.so`` is missing, every call raises.
 
-The names mirror the C ABI in ``include/vsa.h``.
+The names mirror the C ABI in ``include/vsa.h`` and ``include/vsa_block.h``.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import numpy as np
 import torch
@@ -35,6 +35,15 @@ EXPORTS = ("vsa_plan_create", "vsa_plan_info", "vsa_plan_tables", "vsa_keep_coun
            "vsa_runner_create", "vsa_runner_run", "vsa_runner_elapsed", "vsa_runner_destroy",
            "vsa_debug_set_wait_limit", "vsa_sync_status", "vsa_last_error")
 
+# those of include/vsa_block.h
+BLOCK_EXPORTS = ("vsa_rope_create", "vsa_rope_tables", "vsa_rope_destroy", "vsa_rope_apply",
+                 "vsa_norm_rope", "vsa_norm_rope_permute_pool",
+                 "vsa_norm_rope_backward_workspace_size", "vsa_norm_rope_backward", "vsa_linear",
+                 "vsa_linear_backward_workspace_size", "vsa_linear_backward", "vsa_act_backward")
+
+ACTS = {"identity": 0, "sigmoid": 1, "gelu_tanh": 2, "silu": 3}
+MAX_HEAD_TENSORS = 4
+
 
 class VsaError(RuntimeError):
     def __init__(self, status: int, message: str):
@@ -46,6 +55,43 @@ class _Geometry(ctypes.Structure):
     _fields_ = [("n_prefix_segments", ctypes.c_int32), ("prefix_lens", ctypes.POINTER(ctypes.c_int64)),
                 ("grid_t", ctypes.c_int32), ("grid_h", ctypes.c_int32), ("grid_w", ctypes.c_int32),
                 ("tile_t", ctypes.c_int32), ("tile_h", ctypes.c_int32), ("tile_w", ctypes.c_int32)]
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
+
+
+class _RopeDesc(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32 * 3), ("halves", ctypes.c_int32), ("theta", ctypes.c_double * 3),
+                ("offset", ctypes.c_double * 3), ("step", ctypes.c_double * 3),
+                ("inv_freq", ctypes.c_void_p), ("prefix_pos", ctypes.c_void_p)]
+
+
+class _HeadTensor(ctypes.Structure):
+    _fields_ = [("x", _View), ("gain", ctypes.c_void_p), ("gain_type", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("rotate", ctypes.c_int32), ("y", _View),
+                ("pooled", ctypes.c_void_p)]
+
+
+class _HeadGrad(ctypes.Structure):
+    _fields_ = [("dy", _View), ("x", _View), ("gain", ctypes.c_void_p), ("gain_type", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("rotate", ctypes.c_int32), ("dx", _View),
+                ("d_gain", ctypes.c_void_p)]
+
+
+class _LinearArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("x_heads", ctypes.c_int32), ("C", ctypes.c_int32),
+                ("y_heads", ctypes.c_int32), ("O", ctypes.c_int32), ("N", ctypes.c_int64), ("x", _View),
+                ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("bias_type", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("residual", _View), ("pre", _View), ("y", _View)]
+
+
+class _LinearGradArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("x_heads", ctypes.c_int32), ("C", ctypes.c_int32),
+                ("y_heads", ctypes.c_int32), ("O", ctypes.c_int32), ("N", ctypes.c_int64), ("dy", _View),
+                ("x", _View), ("w", ctypes.c_void_p), ("x_pre", _View), ("x_act", ctypes.c_int32),
+                ("dx", _View), ("dw", ctypes.c_void_p), ("db", ctypes.c_void_p)]
 
 
 def lib():
@@ -93,6 +139,18 @@ def lib():
             "vsa_runner_destroy": [P],
             "vsa_debug_set_wait_limit": [ctypes.c_uint64],
             "vsa_sync_status": [P, V],
+            "vsa_rope_create": [P, ctypes.POINTER(_RopeDesc), ctypes.POINTER(P)],
+            "vsa_rope_tables": [P, ctypes.POINTER(I32), V],
+            "vsa_rope_destroy": [P],
+            "vsa_rope_apply": [P, P, _View, _View, I, I, I, I, V],
+            "vsa_norm_rope": [P, P, ctypes.POINTER(_HeadTensor), I, F, I, I, I, V],
+            "vsa_norm_rope_permute_pool": [P, P, ctypes.POINTER(_HeadTensor), I, F, I, I, I, V],
+            "vsa_norm_rope_backward_workspace_size": [P, I, I, ctypes.POINTER(Z)],
+            "vsa_norm_rope_backward": [P, P, ctypes.POINTER(_HeadGrad), I, F, I, I, I, I, V, Z, V],
+            "vsa_linear": [P, ctypes.POINTER(_LinearArgs), V],
+            "vsa_linear_backward_workspace_size": [P, I, I64, I, I, ctypes.POINTER(Z)],
+            "vsa_linear_backward": [P, ctypes.POINTER(_LinearGradArgs), V, Z, V],
+            "vsa_act_backward": [P, V, V, I, V, I64, V],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -561,6 +619,347 @@ def vsa_sparse_attn_backward(plan: Plan, q_t, k_t, v_t, d_out_t, topk_idx, k: in
         _ptr(topk_idx) if topk_idx is not None and topk_idx.numel() else None, k, ref, kr,
         _ptr(lse), _ptr(delta), db[0], db[1], db[2], B, H, D, scale, _ptr(out[0]), _ptr(out[1]),
         _ptr(out[2]), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    return out
+
+
+# ------------------------------------------------- the operators around the layer
+# (include/vsa_block.h)
+
+def _on_plan(plan: Plan, t: torch.Tensor, name: str, dtype=torch.bfloat16):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.get_device() != plan.device:
+        raise ValueError(f"{name} must be on the plan's device, cuda:{plan.device}")
+
+
+def _view(plan: Plan, t: Optional[torch.Tensor], name: str, shape) -> _View:
+    """A strided bf16 tensor [B,H,N,D] or [B,N,C] as a vsa_view."""
+    if t is None:
+        return _View(None, 0, 0, 0)
+    _on_plan(plan, t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    s = t.stride()
+    if s[-1] != 1 and t.numel() > 0:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return _View(t.data_ptr(), s[0], s[1] if len(s) == 4 else 0, s[-2])
+
+
+def _vector(plan: Plan, t: Optional[torch.Tensor], name: str, n: int):
+    """A contiguous parameter vector [n], bf16 or fp32: (pointer, type)."""
+    if t is None:
+        return None, 0
+    _on_plan(plan, t, name, torch.bfloat16 if t.dtype == torch.bfloat16 else torch.float32)
+    if tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+    return t.data_ptr(), 1 if t.dtype == torch.float32 else 0
+
+
+def _dense(plan: Plan, t: Optional[torch.Tensor], name: str, dtype, shape):
+    """A contiguous tensor's pointer."""
+    if t is None:
+        return None
+    _on_plan(plan, t, name, dtype)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+class _Out:
+    """Allocates a call's outputs on the stream that will write them."""
+
+    def __init__(self, plan: Plan, stream):
+        self.dev, self.stream = torch.device("cuda", plan.device), stream
+
+    def __call__(self, shape, dtype=torch.bfloat16):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+
+
+class Rope:
+    """Rotary positions of a plan's tokens (owner of a vsa_rope).  ``dims``: channels
+    of the time, height and width axis; ``theta``, ``offset`` and ``step``: one
+    number or one per axis; ``halves``: pairs (p, P + p) in place of neighbours;
+    ``inv_freq``: P frequencies in place of theta's; ``prefix_pos`` [prefix tokens, 3]:
+    positions of the prefix tokens (None: not rotated)."""
+
+    def __init__(self, plan: Plan, dims: Sequence[int], theta=10000.0, offset=0.0, step=1.0,
+                 halves: bool = False, inv_freq=None, prefix_pos=None):
+        def three(x):
+            return (float(x),) * 3 if np.isscalar(x) else tuple(float(v) for v in x)
+        d = _RopeDesc()
+        d.dim[:] = [int(x) for x in dims]
+        d.halves = int(halves)
+        d.theta[:], d.offset[:], d.step[:] = three(theta), three(offset), three(step)
+        keep = []
+        if inv_freq is not None:
+            f = np.ascontiguousarray(inv_freq, dtype=np.float64).reshape(-1)
+            if f.size != sum(d.dim) // 2:
+                raise ValueError(f"inv_freq must have {sum(d.dim) // 2} entries")
+            keep.append(f)
+            d.inv_freq = f.ctypes.data
+        if prefix_pos is not None:
+            pos = np.ascontiguousarray(prefix_pos, dtype=np.float64)
+            if pos.shape != (sum(plan.prefix_lens), 3):
+                raise ValueError(f"prefix_pos must have shape {(sum(plan.prefix_lens), 3)}")
+            if pos.size:
+                keep.append(pos)
+                d.prefix_pos = pos.ctypes.data
+        h = ctypes.c_void_p()
+        _check(lib().vsa_rope_create(plan.handle, ctypes.byref(d), ctypes.byref(h)))
+        self._h, self.n_tokens = h, plan.n_tokens
+        pairs = ctypes.c_int32()
+        _check(lib().vsa_rope_tables(h, ctypes.byref(pairs), None))
+        self.pairs = pairs.value
+
+    @property
+    def handle(self):
+        return self._h
+
+    def tables(self):
+        """(cos, sin) of every token, fp32 [N, P] each."""
+        out = np.empty((self.n_tokens, self.pairs, 2), np.float32)
+        _check(lib().vsa_rope_tables(self._h, None, ctypes.c_void_p(out.ctypes.data)))
+        return out[..., 0], out[..., 1]
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            lib().vsa_rope_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def vsa_rope_apply(plan: Plan, rope: Rope, x: torch.Tensor, y: Optional[torch.Tensor] = None,
+                   inverse: bool = False, stream=None) -> torch.Tensor:
+    """Rotate x [B,H,N,D] (any strides) by its tokens' positions, or back (inverse:
+    the gradient).  ``y`` may be x."""
+    B, H, _, D = x.shape
+    shape = (B, H, plan.n_tokens, D)
+    xv = _view(plan, x, "x", shape)
+    if y is None:
+        y = _Out(plan, stream)(shape)
+    _check(lib().vsa_rope_apply(plan.handle, rope.handle, xv, _view(plan, y, "y", shape), int(inverse),
+                                B, H, D, _stream(stream)))
+    return y
+
+
+class HeadTensor(NamedTuple):
+    """One tensor of vsa_norm_rope: x [B,H,N,D] (any strides), its gain [D] (bf16 or
+    fp32; None: 1), what is done to it, and where the result goes (None: new)."""
+    x: torch.Tensor
+    gain: Optional[torch.Tensor] = None
+    norm: bool = True
+    rotate: bool = True
+    y: Optional[torch.Tensor] = None
+    pooled: Optional[torch.Tensor] = None
+
+
+class HeadGrad(NamedTuple):
+    """One tensor of vsa_norm_rope_backward: its output's gradient, the forward's x and
+    gain (with the norm), and where dx and d_gain go (None: new; d_gain only for a
+    tensor with a gain)."""
+    dy: torch.Tensor
+    x: Optional[torch.Tensor] = None
+    gain: Optional[torch.Tensor] = None
+    norm: bool = True
+    rotate: bool = True
+    dx: Optional[torch.Tensor] = None
+    d_gain: Optional[torch.Tensor] = None
+
+
+def _norm_rope(plan, items, rope, eps, tiled, stream):
+    if not 1 <= len(items) <= MAX_HEAD_TENSORS:
+        raise ValueError(f"1 to {MAX_HEAD_TENSORS} tensors a call")
+    B, H, _, D = items[0].x.shape
+    natural, out = (B, H, plan.n_tokens, D), _Out(plan, stream)
+    arr, res = (_HeadTensor * len(items))(), []
+    for a, it in zip(arr, items):
+        a.x = _view(plan, it.x, "x", natural)
+        a.gain, a.gain_type = _vector(plan, it.gain, "gain", D)
+        a.norm, a.rotate = int(it.norm), int(it.rotate)
+        if tiled:
+            y = out((B, H, plan.n_padded, D)) if it.y is None else it.y
+            pooled = out((B, H, plan.n_tiles, D), torch.float32) if it.pooled is None else it.pooled
+            a.y.ptr = _dense(plan, y, "y", torch.bfloat16, (B, H, plan.n_padded, D))
+            a.pooled = _dense(plan, pooled, "pooled", torch.float32, (B, H, plan.n_tiles, D))
+            res.append((y, pooled))
+        else:
+            y = out(natural) if it.y is None else it.y
+            a.y = _view(plan, y, "y", natural)
+            res.append(y)
+    fn = lib().vsa_norm_rope_permute_pool if tiled else lib().vsa_norm_rope
+    _check(fn(plan.handle, None if rope is None else rope.handle, arr, len(items), eps, B, H, D,
+              _stream(stream)))
+    return res
+
+
+def vsa_norm_rope(plan: Plan, items: Sequence[HeadTensor], rope: Optional[Rope] = None,
+                  eps: float = 1e-6, stream=None) -> list:
+    """RMS norm of every head's row and its rotation in one pass and one launch for up
+    to four tensors.  Returns their y [B,H,N,D]; ``y`` of an item may be its x."""
+    return _norm_rope(plan, items, rope, eps, False, stream)
+
+
+def vsa_norm_rope_permute_pool(plan: Plan, items: Sequence[HeadTensor], rope: Optional[Rope] = None,
+                               eps: float = 1e-6, stream=None) -> list:
+    """vsa_norm_rope fused with vsa_permute_pool: (x_t [B,H,N_pad,D], pooled
+    [B,H,T,D]) of each tensor; Q, K and V of a layer in one launch."""
+    return _norm_rope(plan, items, rope, eps, True, stream)
+
+
+def norm_rope_backward_workspace(plan: Plan, n: int, D: int) -> torch.Tensor:
+    """Workspace of vsa_norm_rope_backward for n tensors (its size comes from
+    vsa_norm_rope_backward_workspace_size)."""
+    b = ctypes.c_size_t()
+    _check(lib().vsa_norm_rope_backward_workspace_size(plan.handle, n, D, ctypes.byref(b)))
+    return torch.empty(max(b.value, 16), dtype=torch.uint8, device=torch.device("cuda", plan.device))
+
+
+def vsa_norm_rope_backward(plan: Plan, items: Sequence[HeadGrad], rope: Optional[Rope] = None,
+                           eps: float = 1e-6, tiled: bool = False, ws: Optional[torch.Tensor] = None,
+                           stream=None) -> list:
+    """Gradients of vsa_norm_rope, or of its permuting form (``tiled``: dy in tile
+    order).  Returns (dx [B,H,N,D], d_gain fp32 [D] or None) of each tensor."""
+    if not 1 <= len(items) <= MAX_HEAD_TENSORS:
+        raise ValueError(f"1 to {MAX_HEAD_TENSORS} tensors a call")
+    B, H, _, D = items[0].dy.shape
+    natural, out = (B, H, plan.n_tokens, D), _Out(plan, stream)
+    arr, res = (_HeadGrad * len(items))(), []
+    for a, it in zip(arr, items):
+        if tiled:
+            a.dy.ptr = _dense(plan, it.dy, "dy", torch.bfloat16, (B, H, plan.n_padded, D))
+        else:
+            a.dy = _view(plan, it.dy, "dy", natural)
+        if it.norm and it.x is None:
+            raise ValueError("the norm's backward needs x")
+        a.x = _view(plan, it.x if it.norm else None, "x", natural)
+        a.gain, a.gain_type = _vector(plan, it.gain, "gain", D)
+        a.norm, a.rotate = int(it.norm), int(it.rotate)
+        dx = out(natural) if it.dx is None else it.dx
+        a.dx = _view(plan, dx, "dx", natural)
+        dg = it.d_gain
+        if dg is None and it.gain is not None:
+            dg = out((D,), torch.float32)
+        a.d_gain = _dense(plan, dg, "d_gain", torch.float32, (D,))
+        res.append((dx, dg))
+    if ws is None:
+        n = ctypes.c_size_t()
+        _check(lib().vsa_norm_rope_backward_workspace_size(plan.handle, len(items), D, ctypes.byref(n)))
+        ws = out((max(n.value, 16),), torch.uint8)
+    _check(lib().vsa_norm_rope_backward(plan.handle, None if rope is None else rope.handle, arr,
+                                        len(items), eps, int(tiled), B, H, D, _ptr(ws),
+                                        ws.numel() * ws.element_size(), _stream(stream)))
+    return res
+
+
+def _act(act) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}")
+    return ACTS[act]
+
+
+def _sides(t: torch.Tensor, name: str):
+    """(B, N, heads, width) of rows [B,N,C] or heads [B,H,N,D]."""
+    if t.dim() == 4:
+        B, H, N, D = t.shape
+        return B, N, H, H * D
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [B,N,C] or [B,H,N,D]")
+    B, N, C = t.shape
+    return B, N, 0, C
+
+
+def vsa_linear(plan: Plan, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               act: str = "identity", residual: Optional[torch.Tensor] = None, y_heads: int = 0,
+               y: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """y = residual + act(x w^T + bias), one kernel.  x: rows [B,N,C] or heads
+    [B,H,N,D] (C = H*D), any strides; w [O,C]; bias [O] bf16 or fp32.  y: rows, or
+    heads where ``y_heads`` (or the given y, residual) says so.  ``pre`` receives
+    x w^T + bias (what the activation's backward reads).  ``residual`` may be y."""
+    B, N, xh, C = _sides(x, "x")
+    O = w.shape[0]
+    like = y if y is not None else residual if residual is not None else pre
+    if like is not None:
+        y_heads = _sides(like, "y")[2]
+    shape = (B, y_heads, N, O // y_heads) if y_heads else (B, N, O)
+    a = _LinearArgs(B=B, x_heads=xh, C=C, y_heads=y_heads, O=O, N=N)
+    a.x = _view(plan, x, "x", x.shape)
+    a.w = _dense(plan, w, "w", torch.bfloat16, (O, C))
+    a.bias, a.bias_type = _vector(plan, bias, "bias", O)
+    a.act = _act(act)
+    a.residual = _view(plan, residual, "residual", shape)
+    a.pre = _view(plan, pre, "pre", shape)
+    if y is None:
+        y = _Out(plan, stream)(shape)
+    a.y = _view(plan, y, "y", shape)
+    _check(lib().vsa_linear(plan.handle, ctypes.byref(a), _stream(stream)))
+    return y
+
+
+def _linear_backward_bytes(plan: Plan, B: int, N: int, C: int, O: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().vsa_linear_backward_workspace_size(plan.handle, B, N, C, O, ctypes.byref(b)))
+    return max(b.value, 16)
+
+
+def linear_backward_workspace(plan: Plan, B: int, N: int, C: int, O: int) -> torch.Tensor:
+    """Workspace of vsa_linear_backward (its size comes from
+    vsa_linear_backward_workspace_size)."""
+    return torch.empty(_linear_backward_bytes(plan, B, N, C, O), dtype=torch.uint8,
+                       device=torch.device("cuda", plan.device))
+
+
+def vsa_linear_backward(plan: Plan, dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                        x_pre: Optional[torch.Tensor] = None, x_act: str = "identity",
+                        dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                        db: Optional[torch.Tensor] = None, need=(True, True, True),
+                        ws: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of x w^T + bias under dy: (dx, dw bf16 [O,C], db fp32 [O]); ``need`` leaves
+    some of them out (None).  With ``x_pre`` (x = x_act(x_pre)) dx is the gradient of
+    x_pre."""
+    B, N, xh, C = _sides(x, "x")
+    _, _, yh, O = _sides(dy, "dy")
+    out = _Out(plan, stream)
+    a = _LinearGradArgs(B=B, x_heads=xh, C=C, y_heads=yh, O=O, N=N)
+    a.dy = _view(plan, dy, "dy", (B, yh, N, O // yh) if yh else (B, N, O))
+    a.x = _view(plan, x, "x", x.shape)
+    a.w = _dense(plan, w, "w", torch.bfloat16, (O, C))
+    a.x_pre = _view(plan, x_pre, "x_pre", x.shape)
+    a.x_act = _act(x_act)
+    if x_pre is None and a.x_act:
+        raise ValueError("x_act needs x_pre")
+    dx = (out(x.shape) if dx is None else dx) if need[0] else None
+    dw = (out((O, C)) if dw is None else dw) if need[1] else None
+    db = (out((O,), torch.float32) if db is None else db) if need[2] else None
+    a.dx = _view(plan, dx, "dx", x.shape)
+    a.dw = _dense(plan, dw, "dw", torch.bfloat16, (O, C))
+    a.db = _dense(plan, db, "db", torch.float32, (O,))
+    if ws is None:
+        ws = out((_linear_backward_bytes(plan, B, N, C, O),), torch.uint8)
+    _check(lib().vsa_linear_backward(plan.handle, ctypes.byref(a), _ptr(ws),
+                                     ws.numel() * ws.element_size(), _stream(stream)))
+    return dx, dw, db
+
+
+def vsa_act_backward(plan: Plan, dy: torch.Tensor, pre: torch.Tensor, act: str,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dy * act'(pre), element by element (contiguous bf16 tensors of one shape)."""
+    d = _dense(plan, dy, "dy", torch.bfloat16, dy.shape)
+    p = _dense(plan, pre, "pre", torch.bfloat16, dy.shape)
+    if out is None:
+        out = _Out(plan, stream)(dy.shape)
+    o = _dense(plan, out, "out", torch.bfloat16, dy.shape)
+    _check(lib().vsa_act_backward(plan.handle, d, p, _act(act), o, dy.numel(), _stream(stream)))
     return out
 
 
