@@ -6,11 +6,12 @@
 //   g = R^T dy;  u = x r;  dx = r (g gain - u mean(g gain u));  d_gain = sum g u
 //
 // HBM-bound: a row is D bf16 (128 or 256 bytes), read once and written once.
-// One warp takes an item (a head's tile, or a run of rows in natural order);
-// D/8 lanes share a row, each with 8 channels in registers, and the row's sums
-// go through shuffles among them.  Items run head by head for the same rows, so
-// that the warps of a block use the same rows of the (cos, sin) tables, which then
-// come from L1, and so that a [B,N,H,D] input is read along its memory.
+// D/8 lanes share a row, each with 8 channels in registers, and the row's sums go
+// through shuffles among them.  A block takes a run of rows (a tile, or rows in natural
+// order) for a group of heads: a lane keeps the cosines and sines of its rows in
+// registers and walks the heads.  The rows of the next heads are on their way meanwhile:
+// each lane copies its own chunks into slots of shared memory that it alone reads, so that
+// kStages heads are in flight with no register held and no barrier.
 //
 // A lane's 8 channels are four pairs of the rotation: 8c .. 8c+7 where pairs are
 // neighbours, and 4c .. 4c+3 with P+4c .. P+4c+3 where they are halves (two 8-byte
@@ -22,10 +23,6 @@
 
 namespace vsa {
 namespace {
-
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kU = 8;                 // rows in flight per lane
 
 struct RopeArgs {
   const float2* tab;
@@ -40,8 +37,8 @@ struct FwdArgs {
   const int32_t* row_src;
   const int32_t* block_len;
   int64_t N;
-  int H, T, R;                        // items per batch element: T of R rows
-  unsigned n_items;
+  int H, T, R;                        // heads; row blocks (tiles) of a batch element, tile rows
+  int group, groups;                  // heads of an item, items of a row block
   float eps;
 };
 
@@ -49,25 +46,33 @@ struct BwdArgs {
   HeadGradArgs t[VSA_MAX_HEAD_TENSORS];
   RopeArgs rope;
   const int32_t* row_src;
-  const int32_t* block_len;
-  int64_t N;
-  int H, T, R;
+  int64_t rows;                       // rows of dy (padded in tile order)
+  int H, T, group, groups;
   unsigned n_items;
   float eps;
   float* partial;                     // [n][gridDim.x][D]
 };
 
-// Not .nc: in-place calls write what other lanes of the launch read.
-__device__ __forceinline__ uint4 load16(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// Copies into shared memory that wait for no register; zeros where the row is not there.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint16_t* p, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(live ? 16 : 0)
+               : "memory");
 }
-__device__ __forceinline__ uint2 load8(const uint16_t* p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+__device__ __forceinline__ void copy8(uint32_t dst, const uint16_t* p, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(p), "r"(live ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ uint4 slot_load(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src)
+               : "memory");
   return v;
 }
 
@@ -104,10 +109,13 @@ struct Lane {
       n_rot = min(4, max(0, P - p0));
     }
   }
-  __device__ __forceinline__ uint4 load(const uint16_t* row) const {
-    if (!kHalves) return load16(row + o0);
-    const uint2 a = load8(row + o0), b = load8(row + o1);
-    return make_uint4(a.x, a.y, b.x, b.y);
+  __device__ __forceinline__ void fetch(uint32_t slot, const uint16_t* row, bool live) const {
+    if (!kHalves) {
+      copy16(slot, row + o0, live);
+    } else {
+      copy8(slot, row + o0, live);
+      copy8(slot + 8, row + o1, live);
+    }
   }
   __device__ __forceinline__ void store(uint16_t* row, const uint4& v) const {
     if (!kHalves) {
@@ -121,6 +129,16 @@ struct Lane {
     *reinterpret_cast<float4*>(row + o0) = make_float4(f[0], f[1], f[2], f[3]);
     *reinterpret_cast<float4*>(row + o1) = make_float4(f[4], f[5], f[6], f[7]);
   }
+  // The lane's own place in shared memory: f, added to what an earlier pass left there.
+  __device__ __forceinline__ void add_f32(float* row, float (&f)[8], bool add) const {
+    if (add) {
+      const float4 a = *reinterpret_cast<const float4*>(row + o0);
+      const float4 b = *reinterpret_cast<const float4*>(row + o1);
+      f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
+      f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
+    }
+    store_f32(row, f);
+  }
   __device__ __forceinline__ void load_gain(const void* gain, int f32, float (&g)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -130,21 +148,26 @@ struct Lane {
                             : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(gain) + d)) << 16);
     }
   }
-  // Turn f by the token's angles.
-  __device__ __forceinline__ void rotate(const RopeArgs& a, int64_t token, float (&f)[8]) const {
-    if (n_rot == 0) return;
-    const int4 off = __ldg(a.tok + token);
+  // The four (cos, sin) of a token; (1, 0) where the pair does not turn.
+  __device__ __forceinline__ void angles(const RopeArgs& a, int32_t token, float2 (&cs)[4]) const {
+    const int4 off = n_rot > 0 && token >= 0 ? __ldg(a.tok + token) : make_int4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i >= n_rot) break;
-      const int p = p0 + i;
-      const int base = p < a.start1 ? off.x : (p < a.start2 ? off.y : off.z);
-      const float2 cs = __ldg(a.tab + base + p);
-      const float s = a.sign * cs.y;
+      cs[i] = make_float2(1.0f, 0.0f);
+      if (i < n_rot && token >= 0) {
+        const int p = p0 + i;
+        cs[i] = __ldg(a.tab + (p < a.start1 ? off.x : (p < a.start2 ? off.y : off.z)) + p);
+        cs[i].y *= a.sign;
+      }
+    }
+  }
+  static __device__ __forceinline__ void rotate(const float2 (&cs)[4], float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       float& u = f[kHalves ? i : 2 * i];
       float& v = f[kHalves ? i + 4 : 2 * i + 1];
-      const float t = fmaf(u, cs.x, -v * s);
-      v = fmaf(u, s, v * cs.x);
+      const float t = fmaf(u, cs[i].x, -v * cs[i].y);
+      v = fmaf(u, cs[i].y, v * cs[i].x);
       u = t;
     }
   }
@@ -157,43 +180,82 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-template <int kD, bool kHalves, bool kTiled>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ FwdArgs a) {
-  constexpr int kCpr = kD / 8, kRpp = 32 / kCpr;
+// Rows of a block: kThreads / (D/8) at a time, kU of them in each lane.
+template <int kD, int kThreads, int kU>
+struct Block {
+  static constexpr int kCpr = kD / 8, kRpp = 32 / kCpr, kWarps = kThreads / 32;
+  static constexpr int kPass = kWarps * kRpp;      // rows side by side
+  static constexpr int kRows = kPass * kU;
+  static constexpr uint32_t kStage = kThreads * kU * 16;   // slots of one tensor's rows
+};
+constexpr int kStages = 3;
+// Heads of a tile item, at most: its column sums (4 KB a head of 128 channels, 64 KB) and the slots
+// (48 KB) leave room for two blocks on an SM.
+constexpr int kMaxGroup = 16;
+
+template <int kD, bool kHalves, bool kTiled, int kThreads, int kU>
+__global__ void __launch_bounds__(kThreads, kTiled ? 2 : 4)
+    norm_rope_kernel(const __grid_constant__ FwdArgs a) {
+  using Bl = Block<kD, kThreads, kU>;
+  constexpr int kCpr = Bl::kCpr;
+  extern __shared__ __align__(16) uint8_t slots[];
+  // tiles: the column sums of each head and warp
+  float* part = reinterpret_cast<float*>(slots + kStages * Bl::kStage);
   const HeadTensorArgs& t = a.t[blockIdx.y];
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Lane<kD, kHalves> ln(lane % kCpr, a.rope.P);
-  const int sub = lane / kCpr;
+  const unsigned g = blockIdx.x % a.groups, bt = blockIdx.x / a.groups;
+  const unsigned ti = bt % a.T, b = bt / a.T;
+  const int h0 = g * a.group, h1 = min(a.H, h0 + a.group);
+  const int R = kTiled ? a.R : Bl::kRows;          // rows of the item, kRows at a time
+  const int64_t first = int64_t(ti) * R;
+  const int n = kTiled ? __ldg(a.block_len + ti) : int(min(int64_t(R), a.N - first));
+  const uint32_t slot = sm100::smem_u32(slots) + threadIdx.x * 16;
+  const bool plain = !t.norm && !t.rotate;
   float gain[8];
   ln.load_gain(t.gain, t.gain_f32, gain);
-  const bool plain = !t.norm && !t.rotate;
-  for (unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5); item < a.n_items;
-       item += gridDim.x * kWarps) {
-    const unsigned h = item % a.H, bt = item / a.H;
-    const unsigned ti = bt % a.T, b = bt / a.T;
-    const int64_t first = int64_t(ti) * a.R;
-    const int n = kTiled ? __ldg(a.block_len + ti) : int(min(int64_t(a.R), a.N - first));
-    const uint16_t* x = t.x + b * t.xb + h * t.xh;
-    uint16_t* y = kTiled ? t.y + ((int64_t(b) * a.H + h) * a.T + ti) * a.R * kD
-                         : t.y + b * t.yb + h * t.yh;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const int rows = kTiled ? a.R : n;
-    for (int r0 = 0; r0 < rows; r0 += kRpp * kU) {
-      uint4 raw[kU];
-      int32_t src[kU];
+  for (int base = 0; base < R; base += Bl::kRows) {
+    const int r0 = base + warp * Bl::kRpp + lane / kCpr;   // this lane's rows: r0 + u * kPass
+    int32_t src[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int r = r0 + u * kRpp + sub;
-        raw[u] = make_uint4(0u, 0u, 0u, 0u);
-        src[u] = -1;
-        if (r < n) {
-          src[u] = kTiled ? __ldg(a.row_src + first + r) : int32_t(first + r);
-          raw[u] = ln.load(x + int64_t(src[u]) * t.xn);
-        }
+    for (int u = 0; u < kU; ++u) {
+      const int r = r0 + u * Bl::kPass;
+      src[u] = r >= n ? -1 : kTiled ? __ldg(a.row_src + first + r) : int32_t(first + r);
+    }
+    const uint16_t* x = t.x + b * t.xb + h0 * t.xh;
+    uint32_t in = 0, out = 0;                      // stage of the next fetch, of the next head
+    int hf = h0;                                   // head of the next fetch
+    const auto fetch = [&]() {
+      if (hf < h1) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          ln.fetch(slot + in * Bl::kStage + u * kThreads * 16, x + max(src[u], 0) * t.xn, src[u] >= 0);
+        x += t.xh;
+        ++hf;
       }
+      copy_commit();                               // a group a step, empty at the end
+      in = in + 1 == kStages ? 0 : in + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+    float2 cs[kU][4];
+    if (t.rotate) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) ln.angles(a.rope, src[u], cs[u]);
+    }
+    uint16_t* y = kTiled ? t.y + (((int64_t(b) * a.H + h0) * a.T + ti) * R + r0) * kD
+                         : t.y + b * t.yb + h0 * t.yh;
+    const int64_t y_head = kTiled ? int64_t(a.T) * R * kD : t.yh;
+    for (int h = h0; h < h1; ++h) {
+      fetch();
+      copy_wait<kStages - 1>();
+      uint4 raw[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) raw[u] = slot_load(slot + out * Bl::kStage + u * kThreads * 16);
+      out = out + 1 == kStages ? 0 : out + 1;
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int r = r0 + u * kRpp + sub;
         float f[8];
         unpack(raw[u], f);
         if (t.norm) {
@@ -204,109 +266,148 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= rs * gain[i];
         }
-        if (t.rotate && src[u] >= 0) ln.rotate(a.rope, src[u], f);
+        if (t.rotate) ln.rotate(cs[u], f);
         if (kTiled) {
-          if (r < n) {
+          // pad rows are zeros, whatever the gain
+          if (src[u] >= 0) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] += f[i];
           }
-          if (r < rows) ln.store(y + int64_t(r) * kD, plain ? raw[u] : pack(f));
-        } else if (r < n) {
-          ln.store(y + int64_t(src[u]) * t.yn, plain ? raw[u] : pack(f));
+          ln.store(y + u * (Bl::kPass * kD), plain || src[u] < 0 ? raw[u] : pack(f));
+        } else if (src[u] >= 0) {
+          ln.store(y + src[u] * t.yn, plain ? raw[u] : pack(f));
         }
       }
-    }
-    if (kTiled) {
+      y += y_head;
+      if (kTiled) {
 #pragma unroll
-      for (int off = kCpr; off < 32; off <<= 1)
+        for (int off = kCpr; off < 32; off <<= 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], off);
-      if (sub == 0) {
-        const float inv = 1.0f / float(n);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] *= inv;
-        ln.store_f32(t.pooled + ((int64_t(b) * a.H + h) * a.T + ti) * kD, acc);
+          for (int i = 0; i < 8; ++i) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], off);
+        if (lane < kCpr) ln.add_f32(part + ((h - h0) * Bl::kWarps + warp) * kD, acc, base > 0);
       }
+    }
+  }
+  if (kTiled) {
+    // the tile's means: the warps' sums, a head after the other
+    __syncthreads();
+    const float inv = 1.0f / float(n);
+    for (int i = threadIdx.x; i < (h1 - h0) * kD; i += kThreads) {
+      const int h = i / kD, d = i % kD;
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < Bl::kWarps; ++w) s += part[(h * Bl::kWarps + w) * kD + d];
+      t.pooled[((int64_t(b) * a.H + h0 + h) * a.T + ti) * kD + d] = s * inv;
     }
   }
 }
 
-template <int kD, bool kHalves, bool kTiled>
-__global__ void __launch_bounds__(kThreads)
+template <int kD, bool kHalves, bool kTiled, int kThreads, int kU>
+__global__ void __launch_bounds__(kThreads, 512 / kThreads)
     norm_rope_backward_kernel(const __grid_constant__ BwdArgs a) {
-  constexpr int kCpr = kD / 8, kRpp = 32 / kCpr;
-  constexpr int kUb = kU / 2;         // two tensors are read, so half the rows in flight
+  using Bl = Block<kD, kThreads, kU>;
+  constexpr int kCpr = Bl::kCpr;
+  extern __shared__ __align__(16) uint8_t slots[];
   const HeadGradArgs& t = a.t[blockIdx.y];
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Lane<kD, kHalves> ln(lane % kCpr, a.rope.P);
-  const int sub = lane / kCpr;
+  const int r0 = warp * Bl::kRpp + lane / kCpr;
   float gain[8], dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   ln.load_gain(t.gain, t.gain_f32, gain);
   const bool plain = !t.norm && !t.rotate;
-  for (unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5); item < a.n_items;
-       item += gridDim.x * kWarps) {
-    const unsigned h = item % a.H, bt = item / a.H;
+  const uint32_t slot = sm100::smem_u32(slots) + threadIdx.x * 16;
+  uint32_t in = 0, out = 0;
+  for (unsigned item = blockIdx.x; item < a.n_items; item += gridDim.x) {
+    const unsigned g = item % a.groups, bt = item / a.groups;
     const unsigned ti = bt % a.T, b = bt / a.T;
-    const int64_t first = int64_t(ti) * a.R;
-    const int n = kTiled ? __ldg(a.block_len + ti) : int(min(int64_t(a.R), a.N - first));
-    const uint16_t* x = t.x + b * t.xb + h * t.xh;
-    const uint16_t* dy = kTiled ? t.dy + ((int64_t(b) * a.H + h) * a.T + ti) * a.R * kD
-                                : t.dy + b * t.gb + h * t.gh;
-    uint16_t* dx = t.dx + b * t.db + h * t.dh;
-    for (int r0 = 0; r0 < n; r0 += kRpp * kUb) {
-      uint4 rg[kUb], rx[kUb];
-      int32_t src[kUb];
+    const int h0 = g * a.group, h1 = min(a.H, h0 + a.group);
+    const int64_t first = int64_t(ti) * Bl::kRows;
+    int32_t src[kU];
 #pragma unroll
-      for (int u = 0; u < kUb; ++u) {
-        const int r = r0 + u * kRpp + sub;
-        rg[u] = rx[u] = make_uint4(0u, 0u, 0u, 0u);
-        src[u] = -1;
-        if (r < n) {
-          src[u] = kTiled ? __ldg(a.row_src + first + r) : int32_t(first + r);
-          rg[u] = ln.load(dy + (kTiled ? int64_t(r) * kD : int64_t(src[u]) * t.gn));
-          if (t.norm) rx[u] = ln.load(x + int64_t(src[u]) * t.xn);
+    for (int u = 0; u < kU; ++u) {
+      const int64_t r = first + r0 + u * Bl::kPass;
+      src[u] = r >= a.rows ? -1 : kTiled ? __ldg(a.row_src + r) : int32_t(r);
+    }
+    // dy of row u: at tile row first + r, or at the token
+    const uint16_t* dy = kTiled ? t.dy + ((int64_t(b) * a.H + h0) * a.rows + first) * kD
+                                : t.dy + b * t.gb + h0 * t.gh;
+    const int64_t dy_head = kTiled ? a.rows * kD : t.gh;
+    const uint16_t* x = t.x + b * t.xb + h0 * t.xh;
+    uint16_t* dx = t.dx + b * t.db + h0 * t.dh;
+    int hf = h0;
+    const auto fetch = [&]() {
+      if (hf < h1) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const uint32_t s = slot + in * (2 * Bl::kStage) + u * kThreads * 16;
+          const bool live = src[u] >= 0;
+          const int64_t row = max(src[u], 0);
+          ln.fetch(s, kTiled ? dy + (live ? (r0 + u * Bl::kPass) * kD : 0) : dy + row * t.gn, live);
+          if (t.norm) ln.fetch(s + Bl::kStage, x + row * t.xn, live);
         }
+        dy += dy_head;
+        x += t.xh;
+        ++hf;
       }
+      copy_commit();
+      in = in + 1 == kStages ? 0 : in + 1;
+    };
 #pragma unroll
-      for (int u = 0; u < kUb; ++u) {
-        float g[8];
-        unpack(rg[u], g);
-        if (t.rotate && src[u] >= 0) ln.rotate(a.rope, src[u], g);
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+    float2 cs[kU][4];
+    if (t.rotate) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) ln.angles(a.rope, src[u], cs[u]);
+    }
+    for (int h = h0; h < h1; ++h) {
+      fetch();
+      copy_wait<kStages - 1>();
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t s = slot + out * (2 * Bl::kStage) + u * kThreads * 16;
+        const uint4 rg = slot_load(s);
+        float gr[8];
+        unpack(rg, gr);
+        if (t.rotate) ln.rotate(cs[u], gr);
         if (t.norm) {
           // with r = 1/sqrt(mean(x^2) + eps): sum of g gain u = r * (sum of g gain x)
           float f[8], ss = 0.f, gx = 0.f;
-          unpack(rx[u], f);
+          unpack(slot_load(s + Bl::kStage), f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             ss = fmaf(f[i], f[i], ss);
-            gx = fmaf(g[i] * gain[i], f[i], gx);
+            gx = fmaf(gr[i] * gain[i], f[i], gx);
           }
           const float rs = rsqrtf(fmaf(row_sum<kCpr>(ss), 1.0f / kD, a.eps));
           const float m = row_sum<kCpr>(gx) * rs * (1.0f / kD);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float un = f[i] * rs;
-            dw[i] = fmaf(g[i], un, dw[i]);
-            g[i] = rs * fmaf(-un, m, g[i] * gain[i]);
+            dw[i] = fmaf(gr[i], un, dw[i]);
+            gr[i] = rs * fmaf(-un, m, gr[i] * gain[i]);
           }
         }
-        if (src[u] >= 0) ln.store(dx + int64_t(src[u]) * t.dn, plain ? rg[u] : pack(g));
+        if (src[u] >= 0) ln.store(dx + src[u] * t.dn, plain ? rg : pack(gr));
       }
+      out = out + 1 == kStages ? 0 : out + 1;
+      dx += t.dh;
     }
+    // the item's last fetches brought nothing; the stages go on from here
+    in = out;
   }
   if (t.d_gain == nullptr) return;
   // the block's sum, by lanes of a channel first and then by warps, in a fixed order
-  __shared__ float part[kWarps][kD];
+  __shared__ float part[Bl::kWarps][kD];
 #pragma unroll
   for (int off = kCpr; off < 32; off <<= 1)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[i] += __shfl_xor_sync(0xFFFFFFFFu, dw[i], off);
-  if (sub == 0) ln.store_f32(part[threadIdx.x >> 5], dw);
+  if (lane < kCpr) ln.store_f32(part[warp], dw);
   __syncthreads();
   if (threadIdx.x < kD) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += part[w][threadIdx.x];
+    for (int w = 0; w < Bl::kWarps; ++w) s += part[w][threadIdx.x];
     a.partial[(int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kD + threadIdx.x] = s;
   }
 }
@@ -337,7 +438,9 @@ __global__ void __launch_bounds__(1024) gain_sum_kernel(const float* partial, in
   }
 }
 
-int max_blocks(const vsa_plan_s* p) { return (p->num_sms > 0 ? p->num_sms : 148) * 8; }
+int sms(const vsa_plan_s* p) { return p->num_sms > 0 ? p->num_sms : 148; }
+// Blocks of a tensor in the backward, at most: two of 256 threads an SM.
+int max_blocks(const vsa_plan_s* p) { return sms(p) * 2; }
 
 RopeArgs rope_args(const vsa_rope_s* r, int inverse) {
   RopeArgs a = {};
@@ -352,19 +455,35 @@ RopeArgs rope_args(const vsa_rope_s* r, int inverse) {
   return a;
 }
 
-// Rows of an item and items per batch element.
+// Heads of an item.  An item costs its heads and a start of about two more; the blocks
+// come in waves of `slots`: the group that makes the waves shortest.
 template <class Args>
-bool set_items(Args* a, const vsa_plan_s* p, bool tiled, int natural_rows, int B, int H) {
+bool set_items(Args* a, const vsa_plan_s* p, int64_t row_blocks, int B, int H, int n, int64_t slots,
+               int max_group, int64_t* items) {
   a->row_src = p->d_row_src;
-  a->block_len = p->d_block_len;
-  a->N = p->n_tokens;
   a->H = H;
-  a->R = tiled ? p->R : natural_rows;
-  const int64_t T = tiled ? p->n_tiles : (p->n_tokens + a->R - 1) / a->R;
-  a->T = int(T);
-  const int64_t items = int64_t(B) * H * T;
-  a->n_items = unsigned(items);
-  return items < (int64_t(1) << 31);
+  a->T = int(row_blocks);
+  int64_t best = -1;
+  for (int g = 1; g <= std::min(H, max_group); ++g) {
+    const int64_t groups = (H + g - 1) / g;
+    const int64_t cost = (int64_t(B) * row_blocks * n * groups + slots - 1) / slots * (g + 2);
+    if (best < 0 || cost < best) {
+      best = cost;
+      a->group = g;
+      a->groups = int(groups);
+    }
+  }
+  *items = int64_t(B) * row_blocks * a->groups;
+  return *items < (int64_t(1) << 31) && row_blocks < (int64_t(1) << 31);
+}
+
+template <class Kernel, class Args>
+cudaError_t launch(Kernel k, int64_t items, int n, int threads, uint32_t smem, const Args& a,
+                   cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  k<<<dim3(unsigned(items), unsigned(n)), threads, smem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -376,22 +495,35 @@ vsa_status launch_norm_rope(const vsa_plan_s* p, const vsa_rope_s* rope, const H
   for (int i = 0; i < n; ++i) a.t[i] = t[i];
   a.rope = rope_args(rope, inverse);
   a.eps = eps;
-  if (!set_items(&a, p, tiled, kU * 256 / D, B, H))
+  a.block_len = p->d_block_len;
+  a.N = p->n_tokens;
+  // rows of an item: a tile, or 32 (64 of 64 channels) in natural order
+  const int64_t row_blocks = tiled ? p->n_tiles : (p->n_tokens + 4096 / D - 1) / (4096 / D);
+  a.R = p->R;
+  int64_t items = 0;
+  if (!set_items(&a, p, row_blocks, B, H, n, int64_t(sms(p)) * (tiled ? 2 : 4),
+                 tiled ? kMaxGroup : H, &items))
     return fail(VSA_ERR_UNSUPPORTED, "too many heads and rows for one launch");
-  const int64_t want = (int64_t(a.n_items) + kWarps - 1) / kWarps;
-  const dim3 grid(unsigned(std::min<int64_t>(want, max_blocks(p))), unsigned(n));
   const bool halves = rope != nullptr && rope->halves;
-#define VSA_LAUNCH(DD, HV, TL) norm_rope_kernel<DD, HV, TL><<<grid, kThreads, 0, stream>>>(a)
-#define VSA_PICK(DD)                                                     \
-  (halves ? (tiled ? (VSA_LAUNCH(DD, true, true), 0) : (VSA_LAUNCH(DD, true, false), 0)) \
-          : (tiled ? (VSA_LAUNCH(DD, false, true), 0) : (VSA_LAUNCH(DD, false, false), 0)))
-  if (D == 128)
-    (void)VSA_PICK(128);
-  else
-    (void)VSA_PICK(64);
-#undef VSA_PICK
+  cudaError_t e;
+#define VSA_LAUNCH(DD, TL, U)                                                                     \
+  {                                                                                               \
+    const uint32_t smem = kStages * Block<DD, 256, U>::kStage + (TL ? a.group * 8 * DD * 4 : 0);  \
+    e = halves ? launch(norm_rope_kernel<DD, true, TL, 256, U>, items, n, 256, smem, a, stream)   \
+               : launch(norm_rope_kernel<DD, false, TL, 256, U>, items, n, 256, smem, a, stream); \
+  }
+  if (D == 128) {
+    if (tiled)
+      VSA_LAUNCH(128, true, 4)
+    else
+      VSA_LAUNCH(128, false, 2)
+  } else {
+    if (tiled)
+      VSA_LAUNCH(64, true, 2)
+    else
+      VSA_LAUNCH(64, false, 2)
+  }
 #undef VSA_LAUNCH
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VSA_OK
                           : fail(VSA_ERR_CUDA, std::string("norm_rope launch: ") + cudaGetErrorString(e));
 }
@@ -414,24 +546,33 @@ vsa_status launch_norm_rope_backward(const vsa_plan_s* p, const vsa_rope_s* rope
   a.rope = rope_args(rope, 1);
   a.eps = eps;
   a.partial = static_cast<float*>(ws);
-  if (!set_items(&a, p, tiled, kU * 256 / D, B, H))
+  a.rows = tiled ? p->n_padded : p->n_tokens;
+  int64_t items = 0;
+  if (!set_items(&a, p, (a.rows + 63) / 64, B, H, n, max_blocks(p), H, &items))
     return fail(VSA_ERR_UNSUPPORTED, "too many heads and rows for one launch");
-  const int64_t want = (int64_t(a.n_items) + kWarps - 1) / kWarps;
-  const dim3 grid(unsigned(std::min<int64_t>(want, max_blocks(p))), unsigned(n));
+  a.n_items = unsigned(items);
+  const int64_t blocks = std::min<int64_t>(items, max_blocks(p));
   const bool halves = rope != nullptr && rope->halves;
-#define VSA_LAUNCH(DD, HV, TL) norm_rope_backward_kernel<DD, HV, TL><<<grid, kThreads, 0, stream>>>(a)
-#define VSA_PICK(DD)                                                     \
-  (halves ? (tiled ? (VSA_LAUNCH(DD, true, true), 0) : (VSA_LAUNCH(DD, true, false), 0)) \
-          : (tiled ? (VSA_LAUNCH(DD, false, true), 0) : (VSA_LAUNCH(DD, false, false), 0)))
-  if (D == 128)
-    (void)VSA_PICK(128);
-  else
-    (void)VSA_PICK(64);
-#undef VSA_PICK
+  cudaError_t e;
+#define VSA_LAUNCH(DD, TL, U)                                                                  \
+  e = halves ? launch(norm_rope_backward_kernel<DD, true, TL, 256, U>, blocks, n, 256,         \
+                      2 * kStages * Block<DD, 256, U>::kStage, a, stream)                      \
+             : launch(norm_rope_backward_kernel<DD, false, TL, 256, U>, blocks, n, 256,        \
+                      2 * kStages * Block<DD, 256, U>::kStage, a, stream)
+  if (D == 128) {
+    if (tiled)
+      VSA_LAUNCH(128, true, 4);
+    else
+      VSA_LAUNCH(128, false, 4);
+  } else {
+    if (tiled)
+      VSA_LAUNCH(64, true, 2);
+    else
+      VSA_LAUNCH(64, false, 2);
+  }
 #undef VSA_LAUNCH
-  cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && gains) {
-    gain_sum_kernel<<<dim3(D / 32, n), 1024, 0, stream>>>(a.partial, int(grid.x), D, out);
+    gain_sum_kernel<<<dim3(D / 32, n), 1024, 0, stream>>>(a.partial, int(blocks), D, out);
     e = cudaGetLastError();
   }
   return e == cudaSuccess ? VSA_OK
