@@ -11,12 +11,17 @@
 // and write head layouts and strided tensors through the TMA maps and the
 // epilogue's addresses; a 64-column block never crosses a head (D is 64 or 128).
 //
-// Design as in the head projection: one persistent CTA per SM over 256 x 256 output
-// tiles; warp 0 loads 64-wide K blocks of both operands (32 + 32 KB, 128-byte
-// swizzle) into a 3-stage ring by TMA, one lane of warp 1 issues M = 128, N = 256
-// tcgen05.mma into a 2 x 256-column TMEM accumulator (all of it), warps 2-9 take the
-// accumulator out, a row per thread.  Column tiles go in groups whose B rows take at
-// most 32 MB.  Every wait is bounded (abort flag and status word).
+// Design: pairs of CTAs (a cluster of two SMs) over output tiles of 256 rows x 256 or 128
+// columns, persistent.  Each CTA loads its half of the A rows and of the B columns of a
+// 64-wide K block (16 + 16 KB, 128-byte swizzle) into a 6-stage ring by TMA; one lane of the
+// leading CTA issues tcgen05.mma.cta_group::2, M = 256, for both; each CTA has its 128 rows of
+// the accumulator in its own TMEM, twice (2 x 256 columns), so that the epilogue of a
+// tile (biases, activations, residuals) runs under the products of the next.  Epilogue warps
+// pass the accumulator through 2 KB of shared memory of their own, and read residuals and
+// write results in whole 64-byte row pieces.
+//
+// Every wait is bounded (abort flag and status word); the pair meets at cluster
+// barriers before its first and after its last signal.
 #include <algorithm>
 
 #include "block_internal.h"
@@ -26,15 +31,15 @@ namespace vsa {
 namespace {
 using namespace sm100;
 
-constexpr int kBM = 256, kBN = 256, kBK = 64, kStages = 3;
+constexpr int kBM = 256, kBK = 64, kStages = 6;
 constexpr int kThreads = 320;                     // TMA, MMA, 8 epilogue warps
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kHalfA = 128 * kBK * 2;             // rows 128-255 of the tile, in both orders
+constexpr int kABytes = 128 * kBK * 2;            // a CTA's half of the A block
+constexpr int kStageBytes = 2 * kABytes;          // and at most as much of B
 constexpr int kMnAtom = 64 * kBK * 2;             // one 64-column x 64-row box
-constexpr int kNBar = 2 * kStages + 3;            // full[S], empty[S], acc_full, acc_empty, drain
-// stages, barriers, TMEM slot and abort flag, then each epilogue warp's copy of the tile's biases
-constexpr size_t kSmem = size_t(kStages) * kStageBytes + kNBar * 8 + 16 + 8 * kBN * 4 + 1024;
+constexpr int kStaging = 8 * 32 * 64;             // each epilogue warp's 32 rows x 64 bytes
+// full[S], empty[S], acc_full[2], acc_empty[2], drain
+constexpr int kNBar = 2 * kStages + 5;
+constexpr size_t kSmem = size_t(kStages) * kStageBytes + kStaging + 8 * 128 * 4 + kNBar * 8 + 8 + 1024;
 
 enum Order { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
@@ -52,6 +57,7 @@ struct OutView {
 
 struct GemmArgs {
   unsigned int* status;
+  int bn;                          // columns of a tile: 256 or 128
   int m_tiles, n_tiles, group;     // output tiles and the column group of the order
   int k_blocks, k_split, splits;   // K blocks, and how many one split takes
   int rows_b;                      // row blocks (tiles, or K blocks in wgrad) per batch element
@@ -67,12 +73,64 @@ struct GemmArgs {
   float* partial;                  // wgrad with splits > 1: fp32 [splits][M][cols]
 };
 
+// The barrier may be the other CTA's.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int c0, int c1, int c2, int c3) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// wait_bar by a whole warp.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned int* status, unsigned int where) {
+  return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort_flag, status, where));
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The leading CTA's copy of a shared address.
+__device__ __forceinline__ uint32_t at_leader(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this place in both CTAs once the products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar),
+      "h"(uint16_t(3))
       : "memory");
 }
 
@@ -145,39 +203,49 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
                     pack_bf16(f[6], f[7]));
 }
 
-// 64 columns from col of a view's row (column blocks of 64 lie within a head).
-__device__ __forceinline__ uint16_t* out_row(const OutView& v, int64_t b, int64_t n, int col) {
+// Column col of a view (a block of 64 columns lies within a head), less its row.
+__device__ __forceinline__ int64_t col_offset(const OutView& v, int col) {
   const int h = col / v.D;
-  return v.ptr + b * v.sb + h * v.sh + n * v.sn + (col - h * v.D);
+  return h * v.sh + (col - h * v.D);
+}
+
+// An epilogue warp's 32 x 64 bytes of shared memory: 16-byte chunk q of row r at chunk q ^ (r/2 & 3),
+// so that neither a lane per row nor four lanes per row meet in a bank.
+__device__ __forceinline__ uint4* chunk_at(uint8_t* staging, int r, int q) {
+  return reinterpret_cast<uint4*>(staging + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
 }
 
 template <int kOrder>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                   const __grid_constant__ GemmArgs a) {
   constexpr bool kAMn = kOrder == kWgrad, kBMn = kOrder != kForward;
-  constexpr uint32_t kIdesc = idesc_bf16(128, kBN, kAMn, kBMn);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t s_base = smem_u32(smem);
-  const uint32_t bar0 = s_base + kStages * kStageBytes;
-  const uint32_t full = bar0, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
-                 acc_empty = acc_full + 8, drain = acc_empty + 8;
-  uint8_t* tail = smem + kStages * kStageBytes + kNBar * 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
-  float* s_bias = reinterpret_cast<float*>(tail + 16 - (kNBar * 8) % 16);   // 16-byte aligned
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* staging = smem + kStages * kStageBytes;
+  float* s_bias = reinterpret_cast<float*>(staging + kStaging);
+  uint8_t* tail = staging + kStaging + 8 * 128 * 4;
+  const uint32_t full = smem_u32(tail), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
+                 acc_empty = acc_full + 16, drain = acc_empty + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + kNBar * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + kNBar * 8 + 4);
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0);
+  const int rank = int(cluster_rank());
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles = a.m_tiles * a.n_tiles * a.splits;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + 8 * s, 1);
-      mbar_init(empty + 8 * s, 1);
+      mbar_init(full + 8 * s, 1);      // the leader's: its producer, and both CTAs' bytes
+      mbar_init(empty + 8 * s, 1);     // each CTA's own: the commit
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 256);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_empty + 8 * i, 16);  // the leader's: 8 epilogue warps of both CTAs
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -187,229 +255,313 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_b);
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
                  "r"(512u)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                      // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA
-    if (lane == 0) {
-      uint32_t g = 0;
+    // The whole warp walks the blocks and one lane issues: what the instructions need is then
+    // uniform, and stands in uniform registers.  (One lane alone on the loop took
+    // some 100 cycles for every product and copy.)
+    {
+      // The block index is split into coordinates step by step, with no division on the way: a K
+      // block of products takes 512 cycles, and a division by a variable some hundred.
+      uint32_t g = 0, s = 0, phase = 1;  // K block, its stage, parity of the stage's last use
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const int half = a.bn / 2;         // this CTA's columns of the B block
+      const uint32_t lead = at_leader(full);
+      for (int t = pair; t < tiles && ok; t += pairs) {
         int m, n;
         const int sp = t % a.splits;
         decode(t / a.splits, a, m, n);
+        const int b0 = n * a.bn + rank * half;
         const int k0 = sp * a.k_split, k1 = min(a.k_blocks, k0 + a.k_split);
+        // along K: block `i` of `per` in head (or batch element) `o`
+        const int per = kAMn ? a.rows_b : a.ac.blocks;
+        int o = k0 / per, i = k0 - o * per;
+        // across K: boxes of 64 columns (wgrad), or the tile's rows
+        int ca[2] = {0, 0}, ha[2] = {0, 0}, cb[2] = {0, 0}, hb[2] = {0, 0};
+        if (kAMn) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int c = m * kBM + rank * 128 + 64 * j, d = b0 + 64 * j;
+            ha[j] = c / a.ac.D;
+            ca[j] = c - ha[j] * a.ac.D;
+            hb[j] = d / a.bc.D;
+            cb[j] = d - hb[j] * a.bc.D;
+          }
+        } else {
+          ha[0] = m / a.rows_b;
+          ca[0] = (m - ha[0] * a.rows_b) * kBM + rank * 128;
+        }
         for (int kb = k0; kb < k1; ++kb, ++g) {
-          const uint32_t s = g % kStages;
-          if (g >= uint32_t(kStages) &&
-              !wait_bar(empty + 8 * s, ((g / kStages) - 1) & 1, abort_flag, a.status, 31)) {
+          if (g >= uint32_t(kStages) && !wait_warp(empty + 8 * s, phase, abort_flag, a.status, 31)) {
             ok = false;
             break;
           }
-          const uint32_t sa = s_base + s * kStageBytes, sb = sa + kABytes, bar = full + 8 * s;
-          mbar_expect_tx(bar, kStageBytes);
-          if (!kAMn) {
-            // row tile m, K block kb of A's columns
-            const int h = kb / a.ac.blocks, d0 = (kb % a.ac.blocks) * kBK;
-            tma_load_4d(sa, &tm_a, bar, d0, (m % a.rows_b) * kBM, h, m / a.rows_b);
-            const int k = h * a.ac.D + d0;
-            if (!kBMn) {
-              tma_load_4d(sb, &tm_b, bar, k, n * kBN, 0, 0);
+          const uint32_t sa = s_base + s * kStageBytes, sb = sa + kABytes, bar = lead + 8 * s;
+          if (elect_one()) {
+            if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * (kABytes + half * kBK * 2));
+            if (!kAMn) {
+              tma_load_4d(sa, &tm_a, bar, i * kBK, ca[0], o, ha[0]);
+              const int k = o * a.ac.D + i * kBK;
+              if (!kBMn) {
+                tma_load_4d(sb, &tm_b, bar, k, b0, 0, 0);
+              } else {
+                tma_load_4d(sb, &tm_b, bar, b0, k, 0, 0);
+                if (half > 64) tma_load_4d(sb + kMnAtom, &tm_b, bar, b0 + 64, k, 0, 0);
+              }
             } else {
-#pragma unroll
-              for (int i = 0; i < kBN / 64; ++i)
-                tma_load_4d(sb + i * kMnAtom, &tm_b, bar, n * kBN + 64 * i, k, 0, 0);
+              tma_load_4d(sa, &tm_a, bar, ca[0], i * kBK, ha[0], o);
+              tma_load_4d(sa + kMnAtom, &tm_a, bar, ca[1], i * kBK, ha[1], o);
+              tma_load_4d(sb, &tm_b, bar, cb[0], i * kBK, hb[0], o);
+              if (half > 64) tma_load_4d(sb + kMnAtom, &tm_b, bar, cb[1], i * kBK, hb[1], o);
             }
-          } else {
-            const int b = kb / a.rows_b, r0 = (kb % a.rows_b) * kBK;
-#pragma unroll
-            for (int i = 0; i < kBM / 64; ++i) {
-              const int c = m * kBM + 64 * i, h = c / a.ac.D;
-              tma_load_4d(sa + i * kMnAtom, &tm_a, bar, c - h * a.ac.D, r0, h, b);
-            }
-#pragma unroll
-            for (int i = 0; i < kBN / 64; ++i) {
-              const int c = n * kBN + 64 * i, h = c / a.bc.D;
-              tma_load_4d(sb + i * kMnAtom, &tm_b, bar, c - h * a.bc.D, r0, h, b);
-            }
+          }
+          __syncwarp();
+          if (++i == per) {
+            i = 0;
+            ++o;
+          }
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
           }
         }
       }
       if (!ok) {
-        // abort: none of our TMA writes may still be in flight
-        for (uint32_t x = (g > uint32_t(kStages) ? g - kStages : 0); x < g; ++x)
-          wait_bar_drain(full + 8 * (x % kStages), (x / kStages) & 1);
+        // abort: none of our TMA writes may still be in flight.  They complete on the leader's
+        // barriers; the other CTA gives its own a millisecond, some thousand times what
+        // a copy takes
+        if (rank == 0) {
+          for (uint32_t x = (g > uint32_t(kStages) ? g - kStages : 0); x < g; ++x)
+            wait_bar_drain(full + 8 * (x % kStages), (x / kStages) & 1);
+        } else {
+          const unsigned long long t0 = globaltimer();
+          while (globaltimer() - t0 < 1000000ull) {
+          }
+        }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      uint32_t g = 0;
+    // ---------------------------------------------------------------- MMA, for the pair
+    if (rank == 0) {
+      const uint32_t idesc = idesc_bf16(kBM, a.bn, kAMn, kBMn);
+      uint32_t s = 0, phase = 0;
       int lt = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++lt) {
+      for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
         const int k0 = (t % a.splits) * a.k_split;
         const int nk = min(a.k_blocks, k0 + a.k_split) - k0;
-        if (lt >= 1 && !wait_bar(acc_empty, (lt - 1) & 1, abort_flag, a.status, 32)) {
+        const int buf = lt & 1;
+        if (lt >= 2 && !wait_warp(acc_empty + 8 * buf, ((lt >> 1) - 1) & 1, abort_flag, a.status, 32)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        for (int kb = 0; kb < nk && ok; ++kb, ++g) {
-          const uint32_t s = g % kStages;
-          if (!wait_bar(full + 8 * s, (g / kStages) & 1, abort_flag, a.status, 33)) {
+        const uint32_t acc = tmem + buf * 256;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!wait_warp(full + 8 * s, phase, abort_flag, a.status, 33)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sa = s_base + s * kStageBytes, sb = sa + kABytes;
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < kBK / 16; ++ks) {
-            // K-major: 16 columns on; MN-major: 16 rows of 128 bytes on, 64-column atoms
-            // kMnAtom apart
-            const uint64_t bd = kBMn ? sdesc_sw128(sb + ks * 2048, kMnAtom, 1024)
-                                     : sdesc_sw128(sb + ks * 32, 16, 1024);
-            const uint32_t ka = sa + ks * (kAMn ? 2048 : 32);
-            const uint64_t a0 = kAMn ? sdesc_sw128(ka, kMnAtom, 1024) : sdesc_sw128(ka, 16, 1024);
-            const uint64_t a1 = kAMn ? sdesc_sw128(ka + kHalfA, kMnAtom, 1024)
-                                     : sdesc_sw128(ka + kHalfA, 16, 1024);
-            const uint32_t accum = (kb > 0 || ks > 0) ? 1u : 0u;
-            umma_bf16(tmem, a0, bd, kIdesc, accum);
-            umma_bf16(tmem + kBN, a1, bd, kIdesc, accum);
+            for (int ks = 0; ks < kBK / 16; ++ks) {
+              // K-major: 16 columns on; MN-major: 16 rows of 128 bytes on, 64-column atoms
+              // kMnAtom apart
+              const uint64_t ad = kAMn ? sdesc_sw128(sa + ks * 2048, kMnAtom, 1024)
+                                       : sdesc_sw128(sa + ks * 32, 16, 1024);
+              const uint64_t bd = kBMn ? sdesc_sw128(sb + ks * 2048, kMnAtom, 1024)
+                                       : sdesc_sw128(sb + ks * 32, 16, 1024);
+              umma_pair(acc, ad, bd, idesc, (kb > 0 || ks > 0) ? 1u : 0u);
+            }
+            commit_pair(empty + 8 * s);
           }
-          umma_commit(empty + 8 * s);
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
-        if (ok) umma_commit(acc_full);
+        if (ok && elect_one()) commit_pair(acc_full + 8 * buf);
+        __syncwarp();
       }
-      // drain: every MMA issued above complete before TMEM is freed
-      umma_commit(drain);
-      wait_bar_drain(drain, 0);
+      // every product issued above completes before either CTA frees its TMEM
+      if (elect_one()) commit_pair(drain);
+      __syncwarp();
     }
+    if (lane == 0) wait_bar_drain(drain, 0);
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- epilogue
     const int quad = warp & 3;                       // TMEM lane quadrant of this warp
-    const int half = (warp - 2) >> 2;                // rows 0-127 or 128-255 of the tile
-    const int row = half * 128 + quad * 32 + lane;
-    const uint32_t t_row = tmem + (uint32_t(quad * 32) << 16) + uint32_t(half * kBN);
-    float* bias = s_bias + (warp - 2) * kBN;
+    const int side = (warp - 2) >> 2;                // first or second half of the columns
+    const int half = a.bn / 2;
+    uint8_t* st = staging + (warp - 2) * (32 * 64);
+    float* bias = s_bias + (warp - 2) * 128;
+    const int row0 = rank * 128 + quad * 32;         // first row of the warp in the tile
     int lt = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++lt) {
+    for (int t = pair; t < tiles; t += pairs, ++lt) {
       int m, n;
       const int sp = t % a.splits;
       decode(t / a.splits, a, m, n);
-      // this thread's row of the output, as (batch element, row)
-      int64_t r, b, tok;
-      bool live;
-      if (kOrder == kWgrad) {
-        r = int64_t(m) * kBM + row;
-        live = r < a.M;
-        b = 0;
-        tok = r;
-      } else {
-        const int64_t in_b = int64_t(m % a.rows_b) * kBM + row;
-        r = int64_t(m / a.rows_b) * a.N + in_b;
-        live = in_b < a.N;
-        b = r / a.Nrow;
-        tok = r - b * a.Nrow;
+      const int buf = lt & 1;
+      const uint32_t acc = tmem + buf * 256 + (uint32_t(quad * 32) << 16) + uint32_t(side * half);
+      // four lanes write a row's 64 bytes: this lane's rows are 8 i + lane / 4
+      uint32_t tok[4], bat[4];
+      uint32_t live = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int in_tile = row0 + 8 * i + (lane >> 2);
+        if (kOrder == kWgrad) {
+          tok[i] = uint32_t(m) * kBM + in_tile;
+          bat[i] = 0;
+          live |= uint32_t(tok[i] < a.M) << i;
+        } else {
+          const uint32_t in_b = uint32_t(m % a.rows_b) * kBM + in_tile;
+          const uint32_t r = uint32_t(m / a.rows_b) * uint32_t(a.N) + in_b;
+          live |= uint32_t(in_b < a.N) << i;
+          bat[i] = r / uint32_t(a.Nrow);
+          tok[i] = r - bat[i] * uint32_t(a.Nrow);
+        }
       }
+      const int q = lane & 3;                        // and its chunk of them
+      const int col_w = n * a.bn + side * half;      // first column of the warp
       if (kOrder == kForward && a.bias != nullptr) {
-        // the tile's 256 biases, each warp its own copy: no barrier among warps, one of
-        // which may leave the loop on an abort
+        // the warp's biases
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kBN / 32; ++i) {
-          const int col = n * kBN + 32 * i + lane;
+        for (int i = lane; i < half; i += 32) {
           float v = 0.0f;
-          if (col < a.cols)
+          if (col_w + i < a.cols)
             v = a.bias_f32
-                    ? __ldg(static_cast<const float*>(a.bias) + col)
-                    : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.bias) + col)) << 16);
-          bias[32 * i + lane] = v;
+                    ? __ldg(static_cast<const float*>(a.bias) + col_w + i)
+                    : __uint_as_float(
+                          uint32_t(__ldg(static_cast<const uint16_t*>(a.bias) + col_w + i)) << 16);
+          bias[i] = v;
         }
         __syncwarp();
       }
-      if (!__all_sync(0xFFFFFFFFu, wait_bar(acc_full, lt & 1, abort_flag, a.status, 34))) break;
-      tc_fence_after();
-      if (kOrder == kWgrad && a.splits > 1) {
-        float* dst = a.partial + (int64_t(sp) * a.M + r) * a.cols;
-#pragma unroll 1
-        for (int c = 0; c < kBN / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(t_row + 32 * c, v);
-          tmem_wait_ld(v);
-          const int col0 = n * kBN + 32 * c;
+      const bool with_res = kOrder != kWgrad && a.res.ptr != nullptr;
+      uint4 rr[4];
+      const auto load_res = [&](int c) {
+        const int col = col_w + 32 * c + 8 * q;
+        const uint16_t* p = a.res.ptr + (col < a.cols ? col_offset(a.res, col_w + 32 * c) + 8 * q : 0);
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (live && col0 + 4 * q < a.cols)
-              *reinterpret_cast<uint4*>(dst + col0 + 4 * q) =
-                  make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        for (int i = 0; i < 4; ++i) {
+          rr[i] = make_uint4(0u, 0u, 0u, 0u);
+          if ((live >> i & 1) && col < a.cols)
+            rr[i] = *reinterpret_cast<const uint4*>(p + bat[i] * a.res.sb + tok[i] * a.res.sn);
         }
-        tc_fence_before();
-        mbar_arrive(acc_empty);
-        continue;
-      }
-#pragma unroll 1
-      for (int c = 0; c < kBN / 32; ++c) {
+      };
+      // the warp's 32 rows x 32 columns, from shared memory to the rows of a view
+      const auto store_rows = [&](const OutView& v, int c) {
+        __syncwarp();
+        const int col = col_w + 32 * c + 8 * q;
+        if (col < a.cols) {
+          uint16_t* p = v.ptr + col_offset(v, col_w + 32 * c) + 8 * q;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (live >> i & 1)
+              *reinterpret_cast<uint4*>(p + bat[i] * v.sb + tok[i] * v.sn) =
+                  *chunk_at(st, 8 * i + (lane >> 2), q);
+        }
+        __syncwarp();
+      };
+      if (with_res) load_res(0);                     // on its way under the products
+      if (!__all_sync(0xFFFFFFFFu,
+                      wait_bar(acc_full + 8 * buf, (lt >> 1) & 1, abort_flag, a.status, 34)))
+        break;
+      tc_fence_after();
+      for (int c = 0; c < half / 32; ++c) {
+        if (with_res) {
+          // residuals: rows as they were read -> a row per lane
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *chunk_at(st, 8 * i + (lane >> 2), q) = rr[i];
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) rr[e] = *chunk_at(st, lane, e);
+          __syncwarp();
+        }
         uint32_t v[32];
-        tmem_ld32(t_row + 32 * c, v);
+        tmem_ld32(acc + 32 * c, v);
         tmem_wait_ld(v);
-        if (c == kBN / 32 - 1) {
-          tc_fence_before();
-          mbar_arrive(acc_empty);                      // the MMAs of the next tile may start
+        if (kOrder == kWgrad && a.splits > 1) {
+          // fp32 partial products, 16 columns (64 bytes) at a time
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *chunk_at(st, lane, e) = make_uint4(v[16 * j + 4 * e], v[16 * j + 4 * e + 1],
+                                                  v[16 * j + 4 * e + 2], v[16 * j + 4 * e + 3]);
+            __syncwarp();
+            const int col = col_w + 32 * c + 16 * j + 4 * q;
+            if (col < a.cols) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (live >> i & 1)
+                  *reinterpret_cast<uint4*>(a.partial + (int64_t(sp) * a.M + tok[i]) * a.cols + col) =
+                      *chunk_at(st, 8 * i + (lane >> 2), q);
+            }
+            __syncwarp();
+          }
+          continue;
         }
-        const int col0 = n * kBN + 32 * c;
-        if (!live || col0 >= a.cols) continue;
+        float f[4][8];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e / 8][e % 8] = __uint_as_float(v[e]);
         if (kOrder == kForward && a.bias != nullptr) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            v[e] = __float_as_uint(__uint_as_float(v[e]) + bias[32 * c + e]);
+          for (int e = 0; e < 32; ++e) f[e / 8][e % 8] += bias[32 * c + e];
         }
-        uint16_t* yp = out_row(a.y, b, tok, col0);
-        const uint16_t* rp = nullptr;
-        uint16_t* pp = nullptr;
-        if (kOrder != kWgrad && a.res.ptr != nullptr) rp = out_row(a.res, b, tok, col0);
-        if (kOrder == kForward && a.pre.ptr != nullptr) pp = out_row(a.pre, b, tok, col0);
+        if (kOrder == kForward && a.pre.ptr != nullptr) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (col0 + 8 * q >= a.cols) break;
-          float f[8];
+          for (int e = 0; e < 4; ++e) *chunk_at(st, lane, e) = pack(f[e]);
+          store_rows(a.pre, c);
+        }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q + e]);
-          uint4 rr = make_uint4(0u, 0u, 0u, 0u);
-          if (rp != nullptr) rr = *reinterpret_cast<const uint4*>(rp + 8 * q);
-          float x[8];
-          unpack(rr, x);
-          if (kOrder == kForward) {
-            if (pp != nullptr) *reinterpret_cast<uint4*>(pp + 8 * q) = pack(f);
-            act_run(a.act, f);
+        for (int e = 0; e < 4; ++e) {
+          if (kOrder == kForward) act_run(a.act, f[e]);
+          if (with_res) {
+            float x[8];
+            unpack(rr[e], x);
+            if (kOrder == kForward) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] += x[e];
-          } else if (kOrder == kDgrad && rp != nullptr) {
-            slope_run(a.act, x, f);
+              for (int i = 0; i < 8; ++i) f[e][i] += x[i];
+            } else {
+              slope_run(a.act, x, f[e]);
+            }
           }
-          *reinterpret_cast<uint4*>(yp + 8 * q) = pack(f);
+          *chunk_at(st, lane, e) = pack(f[e]);
         }
+        if (with_res && c + 1 < half / 32) load_res(c + 1);
+        store_rows(a.y, c);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(at_leader(acc_empty + 8 * buf));
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                      // no signal to either CTA is on its way
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
                  : "memory");
   }
 }
@@ -444,7 +596,8 @@ __global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, int64_t N
 #pragma unroll 4
     for (int64_t r = r0 + warp; r < r1; r += 8) {
       const int64_t b = r / Nrow;
-      const uint4 v = *reinterpret_cast<const uint4*>(out_row(dy, b, r - b * Nrow, col));
+      const uint4 v = *reinterpret_cast<const uint4*>(dy.ptr + b * dy.sb + (r - b * Nrow) * dy.sn +
+                                                      col_offset(dy, col));
       float f[8];
       unpack(v, f);
 #pragma unroll
@@ -549,11 +702,23 @@ Cols cols_of(const View& v) { return Cols{v.D, (v.D + kBK - 1) / kBK}; }
 
 int sms(const vsa_plan_s* p) { return p->num_sms > 0 ? p->num_sms : 148; }
 
-// Splits of the rows of a weight gradient: as many as leave every SM a tile of at least
-// 8 K blocks.
+int pairs_of(const vsa_plan_s* p) { return sms(p) / 2; }
+
+// Columns of a tile: 256, or 128 where that shortens the waves of tiles over the pairs of SMs (a
+// tile of 128 columns takes a little more than half the time of one of 256).
+int tile_columns(const vsa_plan_s* p, int64_t m_tiles, int cols) {
+  const int64_t n = pairs_of(p);
+  const int64_t t256 = m_tiles * ((cols + 255) / 256), t128 = m_tiles * ((cols + 127) / 128);
+  return (t128 + n - 1) / n * 11 < (t256 + n - 1) / n * 20 ? 128 : 256;
+}
+
+// Splits of the rows of a weight gradient: as many as leave every pair of SMs a tile of at
+// least 8 K blocks.
 int wgrad_splits(const vsa_plan_s* p, int O, int C, int k_blocks) {
-  const int64_t tiles = int64_t((O + kBM - 1) / kBM) * ((C + kBN - 1) / kBN);
-  return int(std::max<int64_t>(1, std::min<int64_t>(sms(p) / tiles, k_blocks / 8)));
+  const int64_t m_tiles = (O + kBM - 1) / kBM;
+  const int bn = tile_columns(p, m_tiles, C);
+  const int64_t tiles = m_tiles * ((C + bn - 1) / bn);
+  return int(std::max<int64_t>(1, std::min<int64_t>(pairs_of(p) / tiles, k_blocks / 8)));
 }
 
 int row_blocks(const View& v, int rows) { return int((v.N + rows - 1) / rows); }
@@ -578,7 +743,7 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
   a.status = p->d_status;
   const int64_t tiles = int64_t(a.m_tiles) * a.n_tiles * a.splits;
   if (tiles >= (int64_t(1) << 31)) return fail(VSA_ERR_UNSUPPORTED, "too many output tiles");
-  const int grid = int(std::min<int64_t>(tiles, sms(p)));
+  const int grid = 2 * int(std::min<int64_t>(tiles, pairs_of(p)));
   linear_kernel<kOrder><<<grid, kThreads, kSmem, stream>>>(ma, mb, a);
   e = cudaGetLastError();
   return e == cudaSuccess ? VSA_OK
@@ -593,7 +758,8 @@ vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, cudaStre
   GemmArgs a = {};
   a.rows_b = row_blocks(x, kBM);
   a.m_tiles = int(x.B) * a.rows_b;
-  a.n_tiles = (q.O + kBN - 1) / kBN;
+  a.bn = tile_columns(p, a.m_tiles, q.O);
+  a.n_tiles = (q.O + a.bn - 1) / a.bn;
   a.ac = cols_of(x);
   a.k_blocks = x.H * a.ac.blocks;
   a.k_split = a.k_blocks;
@@ -608,7 +774,7 @@ vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, cudaStre
   a.bias = q.bias;
   a.bias_f32 = q.bias_type == VSA_F32;
   a.act = q.act;
-  return launch<kForward>(p, x, kBM, matrix(q.w, q.O, q.C), kBN, a, int64_t(q.O) * q.C * 2, stream);
+  return launch<kForward>(p, x, 128, matrix(q.w, q.O, q.C), a.bn / 2, a, int64_t(q.O) * q.C * 2, stream);
 }
 
 size_t linear_backward_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
@@ -637,7 +803,8 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     GemmArgs a = {};
     a.rows_b = row_blocks(g, kBM);
     a.m_tiles = int(g.B) * a.rows_b;
-    a.n_tiles = (q.C + kBN - 1) / kBN;
+    a.bn = tile_columns(p, a.m_tiles, q.C);
+    a.n_tiles = (q.C + a.bn - 1) / a.bn;
     a.ac = cols_of(g);
     a.k_blocks = g.H * a.ac.blocks;
     a.k_split = a.k_blocks;
@@ -649,7 +816,7 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.y = out_view(q.dx, q.x_heads, q.C);
     a.res = out_view(q.x_pre, q.x_heads, q.C);
     a.act = q.x_act;
-    const vsa_status st = launch<kDgrad>(p, g, kBM, matrix(q.w, q.O, q.C), kBK, a,
+    const vsa_status st = launch<kDgrad>(p, g, 128, matrix(q.w, q.O, q.C), kBK, a,
                                          int64_t(q.O) * q.C * 2, stream);
     if (st != VSA_OK) return st;
   }
@@ -667,7 +834,8 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.k_split = (a.k_blocks + a.splits - 1) / a.splits;
     a.splits = (a.k_blocks + a.k_split - 1) / a.k_split;
     a.m_tiles = (q.O + kBM - 1) / kBM;
-    a.n_tiles = (q.C + kBN - 1) / kBN;
+    a.bn = tile_columns(p, a.m_tiles, q.C);
+    a.n_tiles = (q.C + a.bn - 1) / a.bn;
     a.ac = cols_of(g);
     a.bc = cols_of(x);
     a.N = g.N;
