@@ -52,7 +52,7 @@ struct Cols {
 struct OutView {
   uint16_t* ptr;
   int64_t sb, sh, sn;
-  int D;
+  int shift;      // column >> shift is its head: log2 of a head's 64 or 128 channels, 31 for rows
 };
 
 struct GemmArgs {
@@ -142,71 +142,104 @@ __device__ __forceinline__ void decode(int t, const GemmArgs& a, int& m, int& n)
   n = g * G + r % gw;
 }
 
-// exp(-x) overflows to infinity for x < -88, where 1 / (1 + inf) = 0 is the limit.
-__device__ __forceinline__ float sigmoid_f(float x) {
-  return __fdividef(1.0f, 1.0f + __expf(-x));
+// Two fp32 values at a time: the epilogue's arithmetic is bound by its instructions.
+__device__ __forceinline__ uint64_t bits(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
 }
+__device__ __forceinline__ float2 floats(uint64_t r) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+  return v;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return floats(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return floats(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return floats(r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// 1 / (1 + 2^t): the logistic function of x for t = -x log2(e).  2^t = inf gives 0.
+__device__ __forceinline__ float2 logistic2(float2 t) {
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = add2(e, both(1.0f));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+  return e;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC = 1.5957691216057308f;     // 2 sqrt(2/pi)
-__device__ __forceinline__ float gelu_arg(float x) { return kGeluC * fmaf(0.044715f * x * x, x, x); }
+// sigmoid(kGeluC (x + 0.044715 x^3)): gelu_tanh(x) / x
+__device__ __forceinline__ float2 gelu_gate2(float2 x) {
+  const float2 q = fma2(mul2(x, x), both(-kLog2e * kGeluC * 0.044715f), both(-kLog2e * kGeluC));
+  return logistic2(mul2(x, q));
+}
 
 // f = act(f) for a run of values; the choice is uniform and taken once a run.
 template <int kN>
-__device__ __forceinline__ void act_run(int act, float (&f)[kN]) {
+__device__ __forceinline__ void act_run(int act, float2 (&f)[kN]) {
   if (act == VSA_ACT_GELU_TANH) {
 #pragma unroll
-    for (int e = 0; e < kN; ++e) f[e] *= sigmoid_f(gelu_arg(f[e]));
+    for (int e = 0; e < kN; ++e) f[e] = mul2(f[e], gelu_gate2(f[e]));
   } else if (act == VSA_ACT_SILU) {
 #pragma unroll
-    for (int e = 0; e < kN; ++e) f[e] *= sigmoid_f(f[e]);
+    for (int e = 0; e < kN; ++e) f[e] = mul2(f[e], logistic2(mul2(f[e], both(-kLog2e))));
   } else if (act == VSA_ACT_SIGMOID) {
 #pragma unroll
-    for (int e = 0; e < kN; ++e) f[e] = sigmoid_f(f[e]);
+    for (int e = 0; e < kN; ++e) f[e] = logistic2(mul2(f[e], both(-kLog2e)));
   }
 }
 
+// act'(x) of a pair.
+__device__ __forceinline__ float2 act_slope2(int act, float2 x) {
+  if (act == VSA_ACT_GELU_TANH) {
+    // s is 0 in fp32 for x < -10 and 1 - s for x > 6, so the clamp only keeps an overflow
+    // of the square from meeting that 0
+    const float2 s = gelu_gate2(x);
+    const float2 c = make_float2(fminf(fmaxf(x.x, -20.0f), 20.0f), fminf(fmaxf(x.y, -20.0f), 20.0f));
+    const float2 d = fma2(mul2(c, c), both(kGeluC * 0.134145f), both(kGeluC));
+    return fma2(mul2(mul2(c, s), fma2(s, both(-1.0f), both(1.0f))), d, s);
+  }
+  const float2 s = logistic2(mul2(x, both(-kLog2e)));
+  const float2 t = fma2(s, both(-1.0f), both(1.0f));         // 1 - s
+  return act == VSA_ACT_SILU ? fma2(mul2(x, s), t, s) : mul2(s, t);
+}
 // f *= act'(x).
 template <int kN>
-__device__ __forceinline__ void slope_run(int act, const float (&x)[kN], float (&f)[kN]) {
-  if (act == VSA_ACT_GELU_TANH) {
+__device__ __forceinline__ void slope_run(int act, const float2 (&x)[kN], float2 (&f)[kN]) {
+  if (act == VSA_ACT_IDENTITY) return;
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      // s is 0 in fp32 for x < -10 and 1 - s for x > 6, so the clamp only keeps an overflow
-      // of the square from meeting that 0
-      const float s = sigmoid_f(gelu_arg(x[e])), c = fminf(fmaxf(x[e], -20.0f), 20.0f);
-      f[e] *= fmaf(c * s * (1.0f - s), kGeluC * fmaf(0.134145f * c, c, 1.0f), s);
-    }
-  } else if (act == VSA_ACT_SILU) {
-#pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      const float s = sigmoid_f(x[e]);
-      f[e] *= fmaf(x[e] * s, 1.0f - s, s);
-    }
-  } else if (act == VSA_ACT_SIGMOID) {
-#pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      const float s = sigmoid_f(x[e]);
-      f[e] *= s * (1.0f - s);
-    }
-  }
+  for (int e = 0; e < kN; ++e) f[e] = mul2(f[e], act_slope2(act, x[e]));
 }
 
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+__device__ __forceinline__ void unpack(const uint4& v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = __uint_as_float(w[e] << 16);
-    f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-  }
+  for (int e = 0; e < 4; ++e)
+    f[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                    pack_bf16(f[6], f[7]));
+__device__ __forceinline__ uint4 pack(const float2 (&f)[4]) {
+  return make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y),
+                    pack_bf16(f[3].x, f[3].y));
 }
 
 // Column col of a view (a block of 64 columns lies within a head), less its row.
 __device__ __forceinline__ int64_t col_offset(const OutView& v, int col) {
-  const int h = col / v.D;
-  return h * v.sh + (col - h * v.D);
+  const int h = col >> v.shift;
+  return h * v.sh + (col - (h << v.shift));
 }
 
 // An epilogue warp's 32 x 64 bytes of shared memory: 16-byte chunk q of row r at chunk q ^ (r/2 & 3),
@@ -455,23 +488,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       const bool with_res = kOrder != kWgrad && a.res.ptr != nullptr;
+      const bool with_pre = kOrder == kForward && a.pre.ptr != nullptr;
+      const int chunks = half / 32;
+      // residuals: a chunk of 32 columns is on its way, the first under the products
       uint4 rr[4];
       const auto load_res = [&](int c) {
-        const int col = col_w + 32 * c + 8 * q;
-        const uint16_t* p = a.res.ptr + (col < a.cols ? col_offset(a.res, col_w + 32 * c) + 8 * q : 0);
+        const int col = col_w + 32 * c;
+        if (!with_res || col + 8 * q >= a.cols) return;
+        const uint16_t* p = a.res.ptr + col_offset(a.res, col) + 8 * q;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          rr[i] = make_uint4(0u, 0u, 0u, 0u);
-          if ((live >> i & 1) && col < a.cols)
+        for (int i = 0; i < 4; ++i)
+          if (live >> i & 1)
             rr[i] = *reinterpret_cast<const uint4*>(p + bat[i] * a.res.sb + tok[i] * a.res.sn);
-        }
       };
-      // the warp's 32 rows x 32 columns, from shared memory to the rows of a view
-      const auto store_rows = [&](const OutView& v, int c) {
+      // the warp's 32 rows x 32 columns, a row a lane, through shared memory to the rows of a view
+      const auto store_rows = [&](const OutView& v, int c, const uint4 (&o)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *chunk_at(st, lane, e) = o[e];
         __syncwarp();
-        const int col = col_w + 32 * c + 8 * q;
-        if (col < a.cols) {
-          uint16_t* p = v.ptr + col_offset(v, col_w + 32 * c) + 8 * q;
+        const int col = col_w + 32 * c;
+        if (col + 8 * q < a.cols) {
+          uint16_t* p = v.ptr + col_offset(v, col) + 8 * q;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (live >> i & 1)
@@ -480,26 +517,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      if (with_res) load_res(0);                     // on its way under the products
-      if (!__all_sync(0xFFFFFFFFu,
-                      wait_bar(acc_full + 8 * buf, (lt >> 1) & 1, abort_flag, a.status, 34)))
-        break;
+      // the accumulator is out: the products of the tile after the next may start
+      const auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(at_leader(acc_empty + 8 * buf));
+      };
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rr[i] = make_uint4(0u, 0u, 0u, 0u);
+      load_res(0);
+      if (!wait_warp(acc_full + 8 * buf, (lt >> 1) & 1, abort_flag, a.status, 34)) break;
       tc_fence_after();
-      for (int c = 0; c < half / 32; ++c) {
-        if (with_res) {
-          // residuals: rows as they were read -> a row per lane
-#pragma unroll
-          for (int i = 0; i < 4; ++i) *chunk_at(st, 8 * i + (lane >> 2), q) = rr[i];
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 4; ++e) rr[e] = *chunk_at(st, lane, e);
-          __syncwarp();
-        }
-        uint32_t v[32];
-        tmem_ld32(acc + 32 * c, v);
-        tmem_wait_ld(v);
-        if (kOrder == kWgrad && a.splits > 1) {
-          // fp32 partial products, 16 columns (64 bytes) at a time
+      uint32_t v[32];
+      tmem_ld32(acc, v);
+      if (kOrder == kWgrad && a.splits > 1) {
+        // fp32 partial products, 16 columns (64 bytes) at a time
+        for (int c = 0; c < chunks; ++c) {
+          tmem_wait_ld(v);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -517,41 +551,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
-          continue;
+          if (c + 1 < chunks) tmem_ld32(acc + 32 * c + 32, v);
         }
-        float f[4][8];
+        release();
+        continue;
+      }
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        uint4 x4[4];
+        if (with_res) {
+          // residuals: rows as they were read -> a row per lane
 #pragma unroll
-        for (int e = 0; e < 32; ++e) f[e / 8][e % 8] = __uint_as_float(v[e]);
+          for (int i = 0; i < 4; ++i) *chunk_at(st, 8 * i + (lane >> 2), q) = rr[i];
+          if (c + 1 < chunks) load_res(c + 1);
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x4[e] = *chunk_at(st, lane, e);
+          __syncwarp();
+        }
+        tmem_wait_ld(v);
+        float2 f[4][4];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          f[e / 4][e % 4] = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
         if (kOrder == kForward && a.bias != nullptr) {
+          const float4* bp = reinterpret_cast<const float4*>(bias + 32 * c);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) f[e / 8][e % 8] += bias[32 * c + e];
+          for (int e = 0; e < 8; ++e) {
+            const float4 w = bp[e];
+            float2 &g0 = f[e / 2][2 * (e % 2)], &g1 = f[e / 2][2 * (e % 2) + 1];
+            g0 = add2(g0, make_float2(w.x, w.y));
+            g1 = add2(g1, make_float2(w.z, w.w));
+          }
         }
-        if (kOrder == kForward && a.pre.ptr != nullptr) {
+        uint4 o[4];
+        if (with_pre) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) *chunk_at(st, lane, e) = pack(f[e]);
-          store_rows(a.pre, c);
+          for (int e = 0; e < 4; ++e) o[e] = pack(f[e]);
+          store_rows(a.pre, c, o);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (kOrder == kForward) act_run(a.act, f[e]);
           if (with_res) {
-            float x[8];
-            unpack(rr[e], x);
+            float2 x[4];
+            unpack(x4[e], x);
             if (kOrder == kForward) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) f[e][i] += x[i];
+              for (int i = 0; i < 4; ++i) f[e][i] = add2(f[e][i], x[i]);
             } else {
               slope_run(a.act, x, f[e]);
             }
           }
-          *chunk_at(st, lane, e) = pack(f[e]);
+          o[e] = pack(f[e]);
         }
-        if (with_res && c + 1 < half / 32) load_res(c + 1);
-        store_rows(a.y, c);
+        if (c + 1 < chunks)
+          tmem_ld32(acc + 32 * c + 32, v);
+        else
+          release();
+        store_rows(a.y, c, o);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_at(at_leader(acc_empty + 8 * buf));
     }
   }
 
@@ -598,10 +657,13 @@ __global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, int64_t N
       const int64_t b = r / Nrow;
       const uint4 v = *reinterpret_cast<const uint4*>(dy.ptr + b * dy.sb + (r - b * Nrow) * dy.sn +
                                                       col_offset(dy, col));
-      float f[8];
+      float2 f[4];
       unpack(v, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += f[e];
+      for (int e = 0; e < 4; ++e) {
+        acc[2 * e] += f[e].x;
+        acc[2 * e + 1] += f[e].y;
+      }
     }
   }
 #pragma unroll
@@ -637,7 +699,7 @@ __global__ void __launch_bounds__(256) colsum_join_kernel(const float* part, int
 __global__ void __launch_bounds__(256) act_backward_kernel(const uint4* dy, const uint4* pre, int act,
                                                            uint4* out, int64_t n8) {
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n8; i += int64_t(gridDim.x) * 256) {
-    float g[8], x[8];
+    float2 g[4], x[4];
     unpack(dy[i], g);
     unpack(pre[i], x);
     slope_run(act, x, g);
@@ -695,7 +757,7 @@ View matrix(const void* p, int64_t rows, int cols) {
 
 OutView out_view(const vsa_view& v, int heads, int C) {
   return OutView{static_cast<uint16_t*>(v.ptr), v.stride_b, heads > 0 ? v.stride_h : 0, v.stride_n,
-                 heads > 0 ? C / heads : C};
+                 heads > 0 ? (C / heads == 64 ? 6 : 7) : 31};
 }
 
 Cols cols_of(const View& v) { return Cols{v.D, (v.D + kBK - 1) / kBK}; }
@@ -704,12 +766,13 @@ int sms(const vsa_plan_s* p) { return p->num_sms > 0 ? p->num_sms : 148; }
 
 int pairs_of(const vsa_plan_s* p) { return sms(p) / 2; }
 
-// Columns of a tile: 256, or 128 where that shortens the waves of tiles over the pairs of SMs (a
-// tile of 128 columns takes a little more than half the time of one of 256).
+// Columns of a tile: 256, or 128 where that shortens the waves of tiles over the pairs of SMs.  A
+// tile of 128 columns takes 0.72 of the time of one of 256 (20 of 29 us at K = 5,376, 4.8 of
+// 6.5 us at K = 1,024): its products want half as much again of operand bytes a cycle.
 int tile_columns(const vsa_plan_s* p, int64_t m_tiles, int cols) {
   const int64_t n = pairs_of(p);
   const int64_t t256 = m_tiles * ((cols + 255) / 256), t128 = m_tiles * ((cols + 127) / 128);
-  return (t128 + n - 1) / n * 11 < (t256 + n - 1) / n * 20 ? 128 : 256;
+  return (t128 + n - 1) / n * 18 < (t256 + n - 1) / n * 25 ? 128 : 256;
 }
 
 // Splits of the rows of a weight gradient: as many as leave every pair of SMs a tile of at
@@ -842,7 +905,7 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.M = q.O;
     a.cols = q.C;
     a.Nrow = q.O;
-    a.y = OutView{static_cast<uint16_t*>(q.dw), 0, 0, q.C, q.C};
+    a.y = OutView{static_cast<uint16_t*>(q.dw), 0, 0, q.C, 31};
     a.partial = static_cast<float*>(ws);
     // the rows are long: all column tiles of one group share the pass over them
     const vsa_status st = launch<kWgrad>(p, g, kBK, x, kBK, a, 0, stream);
