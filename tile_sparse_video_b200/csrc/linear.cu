@@ -55,10 +55,28 @@ struct OutView {
   int shift;      // column >> shift is its head: log2 of a head's 64 or 128 channels, 31 for rows
 };
 
+// Division of 0 <= n < 2^31 by a number fixed at launch: n * mul / 2^(32 + shift) with
+// mul = ceil(2^(32 + shift) / d).  mul * d exceeds 2^(32 + shift) by less than
+// d <= 2^(shift + 1), and n times that stays below 2^(32 + shift): the quotient is exact.
+struct Div {
+  uint32_t d, mul, shift;
+};
+__host__ __forceinline__ Div make_div(int64_t d) {
+  Div v = {uint32_t(d), 0, 0};
+  while ((int64_t(2) << v.shift) < d) ++v.shift;
+  v.mul = uint32_t(((uint64_t(1) << (32 + v.shift)) + d - 1) / d);
+  return v;
+}
+__device__ __forceinline__ uint32_t operator/(uint32_t n, const Div& v) {
+  return v.d == 1 ? n : __umulhi(n, v.mul) >> v.shift;
+}
+
 struct GemmArgs {
   unsigned int* status;
   int bn;                          // columns of a tile: 256 or 128
   int m_tiles, n_tiles, group;     // output tiles and the column group of the order
+  Div by_group, by_width, by_last; // tiles of a group; its columns, and the last group's
+  Div by_splits, by_rows_b, by_nrow;
   int k_blocks, k_split, splits;   // K blocks, and how many one split takes
   int rows_b;                      // row blocks (tiles, or K blocks in wgrad) per batch element
   int64_t N;                       // rows of a batch element of the TMA views
@@ -112,8 +130,10 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Relaxed: the accumulator's reads are ordered by the tcgen05 fence before it, and a release at
+// cluster scope would first wait for this thread's stores to global memory (1-2 us a tile).
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
 }
 __device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
@@ -134,12 +154,15 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       : "memory");
 }
 
-__device__ __forceinline__ void decode(int t, const GemmArgs& a, int& m, int& n) {
-  const int G = a.group;
-  const int g = t / (a.m_tiles * G), r = t % (a.m_tiles * G);
-  const int gw = min(G, a.n_tiles - g * G);
-  m = r / gw;
-  n = g * G + r % gw;
+// Work item t -> split, and output tile (m, n): the column tiles in groups, m-major within one.
+__device__ __forceinline__ void decode(int t, const GemmArgs& a, int& sp, int& m, int& n) {
+  const uint32_t tile = uint32_t(t) / a.by_splits;
+  sp = t - int(tile) * a.splits;
+  const uint32_t g = tile / a.by_group, r = tile - g * a.by_group.d;
+  const int first = int(g) * a.group;
+  const bool last = first + a.group >= a.n_tiles;
+  m = int(last ? r / a.by_last : r / a.by_width);
+  n = first + int(r) - m * int(last ? a.by_last.d : a.by_width.d);
 }
 
 // Two fp32 values at a time: the epilogue's arithmetic is bound by its instructions.
@@ -225,13 +248,13 @@ __device__ __forceinline__ void slope_run(int act, const float2 (&x)[kN], float2
   for (int e = 0; e < kN; ++e) f[e] = mul2(f[e], act_slope2(act, x[e]));
 }
 
-__device__ __forceinline__ void unpack(const uint4& v, float2 (&f)[4]) {
+__device__ __forceinline__ void unpack(const uint4& v, float2* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     f[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 pack(const float2 (&f)[4]) {
+__device__ __forceinline__ uint4 pack(const float2* f) {
   return make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y),
                     pack_bf16(f[3].x, f[3].y));
 }
@@ -313,9 +336,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int half = a.bn / 2;         // this CTA's columns of the B block
       const uint32_t lead = at_leader(full);
       for (int t = pair; t < tiles && ok; t += pairs) {
-        int m, n;
-        const int sp = t % a.splits;
-        decode(t / a.splits, a, m, n);
+        int sp, m, n;
+        decode(t, a, sp, m, n);
         const int b0 = n * a.bn + rank * half;
         const int k0 = sp * a.k_split, k1 = min(a.k_blocks, k0 + a.k_split);
         // along K: block `i` of `per` in head (or batch element) `o`
@@ -333,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             cb[j] = d - hb[j] * a.bc.D;
           }
         } else {
-          ha[0] = m / a.rows_b;
+          ha[0] = int(uint32_t(m) / a.by_rows_b);
           ca[0] = (m - ha[0] * a.rows_b) * kBM + rank * 128;
         }
         for (int kb = k0; kb < k1; ++kb, ++g) {
@@ -394,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int lt = 0;
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
-        const int k0 = (t % a.splits) * a.k_split;
+        const int k0 = (t - int(uint32_t(t) / a.by_splits) * a.splits) * a.k_split;
         const int nk = min(a.k_blocks, k0 + a.k_split) - k0;
         const int buf = lt & 1;
         if (lt >= 2 && !wait_warp(acc_empty + 8 * buf, ((lt >> 1) - 1) & 1, abort_flag, a.status, 32)) {
@@ -446,16 +468,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* st = staging + (warp - 2) * (32 * 64);
     float* bias = s_bias + (warp - 2) * 128;
     const int row0 = rank * 128 + quad * 32;         // first row of the warp in the tile
+    float next_bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // column 32 i + lane of the next tile
+    const auto read_bias = [&](int t) {
+      int sp, m, n;
+      decode(t, a, sp, m, n);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = n * a.bn + side * half + 32 * i + lane;
+        next_bias[i] = 0.0f;
+        if (32 * i < half && col < a.cols)
+          next_bias[i] =
+              a.bias_f32 ? __ldg(static_cast<const float*>(a.bias) + col)
+                         : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.bias) + col)) << 16);
+      }
+    };
+    if (kOrder == kForward && a.bias != nullptr && pair < tiles) read_bias(pair);
     int lt = 0;
     for (int t = pair; t < tiles; t += pairs, ++lt) {
-      int m, n;
-      const int sp = t % a.splits;
-      decode(t / a.splits, a, m, n);
+      int sp, m, n;
+      decode(t, a, sp, m, n);
       const int buf = lt & 1;
       const uint32_t acc = tmem + buf * 256 + (uint32_t(quad * 32) << 16) + uint32_t(side * half);
       // four lanes write a row's 64 bytes: this lane's rows are 8 i + lane / 4
       uint32_t tok[4], bat[4];
       uint32_t live = 0;
+      const uint32_t mb = kOrder == kWgrad ? 0 : uint32_t(m) / a.by_rows_b;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int in_tile = row0 + 8 * i + (lane >> 2);
@@ -464,31 +501,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           bat[i] = 0;
           live |= uint32_t(tok[i] < a.M) << i;
         } else {
-          const uint32_t in_b = uint32_t(m % a.rows_b) * kBM + in_tile;
-          const uint32_t r = uint32_t(m / a.rows_b) * uint32_t(a.N) + in_b;
+          const uint32_t in_b = (uint32_t(m) - mb * uint32_t(a.rows_b)) * kBM + in_tile;
+          const uint32_t r = mb * uint32_t(a.N) + in_b;
           live |= uint32_t(in_b < a.N) << i;
-          bat[i] = r / uint32_t(a.Nrow);
+          bat[i] = r / a.by_nrow;
           tok[i] = r - bat[i] * uint32_t(a.Nrow);
         }
       }
       const int q = lane & 3;                        // and its chunk of them
       const int col_w = n * a.bn + side * half;      // first column of the warp
-      if (kOrder == kForward && a.bias != nullptr) {
-        // the warp's biases
+      const bool with_bias = kOrder == kForward && a.bias != nullptr;
+      if (with_bias) {
+        // the tile's biases were read during the tile before
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bias[32 * i + lane] = next_bias[i];
         __syncwarp();
-        for (int i = lane; i < half; i += 32) {
-          float v = 0.0f;
-          if (col_w + i < a.cols)
-            v = a.bias_f32
-                    ? __ldg(static_cast<const float*>(a.bias) + col_w + i)
-                    : __uint_as_float(
-                          uint32_t(__ldg(static_cast<const uint16_t*>(a.bias) + col_w + i)) << 16);
-          bias[i] = v;
-        }
-        __syncwarp();
+        if (t + pairs < tiles) read_bias(t + pairs);
       }
       const bool with_res = kOrder != kWgrad && a.res.ptr != nullptr;
       const bool with_pre = kOrder == kForward && a.pre.ptr != nullptr;
+      // nothing of the warp's rows and columns is over the edge
+      const bool inside = __all_sync(0xFFFFFFFFu, live == 15u) && col_w + half <= a.cols;
       const int chunks = half / 32;
       // residuals: a chunk of 32 columns is on its way, the first under the products
       uint4 rr[4];
@@ -506,14 +539,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) *chunk_at(st, lane, e) = o[e];
         __syncwarp();
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *chunk_at(st, 8 * i + (lane >> 2), q);
         const int col = col_w + 32 * c;
-        if (col + 8 * q < a.cols) {
-          uint16_t* p = v.ptr + col_offset(v, col) + 8 * q;
+        uint16_t* p = v.ptr + col_offset(v, col) + 8 * q;
+        if (inside) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(p + bat[i] * v.sb + tok[i] * v.sn) = w[i];
+        } else if (col + 8 * q < a.cols) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (live >> i & 1)
-              *reinterpret_cast<uint4*>(p + bat[i] * v.sb + tok[i] * v.sn) =
-                  *chunk_at(st, 8 * i + (lane >> 2), q);
+            if (live >> i & 1) *reinterpret_cast<uint4*>(p + bat[i] * v.sb + tok[i] * v.sn) = w[i];
         }
         __syncwarp();
       };
@@ -570,41 +607,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         tmem_wait_ld(v);
-        float2 f[4][4];
+        float2 f[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          f[e / 4][e % 4] = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-        if (kOrder == kForward && a.bias != nullptr) {
+          f[e] = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+        if (with_bias) {
           const float4* bp = reinterpret_cast<const float4*>(bias + 32 * c);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 w = bp[e];
-            float2 &g0 = f[e / 2][2 * (e % 2)], &g1 = f[e / 2][2 * (e % 2) + 1];
-            g0 = add2(g0, make_float2(w.x, w.y));
-            g1 = add2(g1, make_float2(w.z, w.w));
+            f[2 * e] = add2(f[2 * e], make_float2(w.x, w.y));
+            f[2 * e + 1] = add2(f[2 * e + 1], make_float2(w.z, w.w));
           }
         }
         uint4 o[4];
         if (with_pre) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = pack(f[e]);
+          for (int e = 0; e < 4; ++e) o[e] = pack(&f[4 * e]);
           store_rows(a.pre, c, o);
         }
+        if (kOrder == kForward) act_run(a.act, f);
+        if (with_res) {
+          float2 x[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (kOrder == kForward) act_run(a.act, f[e]);
-          if (with_res) {
-            float2 x[4];
-            unpack(x4[e], x);
-            if (kOrder == kForward) {
+          for (int e = 0; e < 4; ++e) unpack(x4[e], &x[4 * e]);
+          if (kOrder == kForward) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) f[e][i] = add2(f[e][i], x[i]);
-            } else {
-              slope_run(a.act, x, f[e]);
-            }
+            for (int e = 0; e < 16; ++e) f[e] = add2(f[e], x[e]);
+          } else {
+            slope_run(a.act, x, f);
           }
-          o[e] = pack(f[e]);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = pack(&f[4 * e]);
         if (c + 1 < chunks)
           tmem_ld32(acc + 32 * c + 32, v);
         else
@@ -803,6 +838,12 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
   if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
   const int64_t groups = std::max<int64_t>(1, (b_bytes + (int64_t(32) << 20) - 1) >> 25);
   a.group = int(std::max<int64_t>(1, (a.n_tiles + groups - 1) / groups));
+  a.by_group = make_div(int64_t(a.m_tiles) * a.group);
+  a.by_width = make_div(a.group);
+  a.by_last = make_div(a.n_tiles - (a.n_tiles - 1) / a.group * a.group);
+  a.by_splits = make_div(a.splits);
+  a.by_rows_b = make_div(a.rows_b);
+  a.by_nrow = make_div(a.Nrow);
   a.status = p->d_status;
   const int64_t tiles = int64_t(a.m_tiles) * a.n_tiles * a.splits;
   if (tiles >= (int64_t(1) << 31)) return fail(VSA_ERR_UNSUPPORTED, "too many output tiles");
