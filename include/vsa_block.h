@@ -155,10 +155,16 @@ typedef struct vsa_linear_args {
   vsa_view y;
 } vsa_linear_args;
 
+/* Bytes of workspace with which vsa_linear splits a product of few rows over more of the GPU
+ * (fp32 partial sums); 0 where it would not.  Nothing in it has to be set. */
+vsa_status vsa_linear_workspace_size(vsa_plan plan, int B, int64_t N, int C, int O, size_t* bytes);
+
 /* y = residual + act(x w^T + bias).  fp32 accumulation and epilogue, one
  * rounding to bf16; pre is rounded on its own.  C and O are multiples of 8.  y
- * and pre must not overlap x or w. */
-vsa_status vsa_linear(vsa_plan plan, const vsa_linear_args* args, void* stream);
+ * and pre must not overlap x or w.  ws: at least vsa_linear_workspace_size bytes,
+ * or NULL: the same result up to fp32 summation order, without the split. */
+vsa_status vsa_linear(vsa_plan plan, const vsa_linear_args* args, void* ws, size_t ws_bytes,
+                      void* stream);
 
 typedef struct vsa_linear_grad_args {
   int32_t B, x_heads, C, y_heads, O;

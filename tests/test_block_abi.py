@@ -89,7 +89,7 @@ def test_host_only_plan_refuses_launches(libvsa):
     assert L.vsa_norm_rope_permute_pool(plan.handle, rope.handle, t, 1, 1e-6, 1, 1, 64, None) == 1
     g = (vsa._HeadGrad * 1)()
     assert L.vsa_norm_rope_backward(plan.handle, rope.handle, g, 1, 1e-6, 0, 1, 1, 64, None, 0, None) == 1
-    assert L.vsa_linear(plan.handle, ctypes.byref(vsa._LinearArgs()), None) == 1
+    assert L.vsa_linear(plan.handle, ctypes.byref(vsa._LinearArgs()), None, 0, None) == 1
     assert L.vsa_linear_backward(plan.handle, ctypes.byref(vsa._LinearGradArgs()), None, 0, None) == 1
     assert L.vsa_act_backward(plan.handle, None, None, 0, None, 8, None) == 1
     assert b"host-only" in L.vsa_last_error()
@@ -104,6 +104,11 @@ def test_host_only_plan_refuses_launches(libvsa):
     assert L.vsa_linear_backward_workspace_size(plan.handle, 1, -1, 64, 64, ctypes.byref(n)) == 1
     assert L.vsa_linear_backward_workspace_size(plan.handle, 1, 64, 60, 64, ctypes.byref(n)) == 1
     assert L.vsa_linear_backward_workspace_size(plan.handle, 1, 64, 64, 64, ctypes.byref(n)) == 0
+    assert L.vsa_linear_workspace_size(plan.handle, 1, 64, 60, 64, ctypes.byref(n)) == 1
+    # one token reads w without a split; 64 rows of 64 K blocks split over the pairs of SMs
+    assert L.vsa_linear_workspace_size(plan.handle, 1, 1, 4096, 256, ctypes.byref(n)) == 0 and n.value == 0
+    assert L.vsa_linear_workspace_size(plan.handle, 1, 64, 4096, 256, ctypes.byref(n)) == 0
+    assert n.value > 0 and n.value % (64 * 256 * 4) == 0
     # the handle does not refer to its plan
     plan.close()
     assert rope.tables()[0].shape == (366, 32)

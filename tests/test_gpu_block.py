@@ -246,6 +246,7 @@ LINEARS = [
     (1, 1, 0, 64, 0, 64), (1, 1, 0, 520, 0, 1032), (3, 1, 0, 8, 0, 8), (2, 1, 2, 128, 3, 192),
     (1, 7, 0, 32, 0, 264), (1, 255, 0, 72, 0, 256), (1, 257, 3, 384, 0, 136), (2, 300, 2, 256, 4, 256),
     (2, 513, 0, 200, 2, 128), (1, 1000, 4, 256, 3, 384), (1, 16, 0, 2048, 0, 40), (1, 33, 0, 264, 5, 640),
+    (2, 4, 3, 384, 0, 72), (3, 3, 0, 1032, 2, 256), (2, 150, 9, 1152, 0, 96), (1, 700, 0, 40, 8, 1024),
 ]
 linears = pytest.mark.parametrize("c", LINEARS, ids=lambda c: "x".join(map(str, c)))
 
@@ -289,6 +290,14 @@ def test_linear(c, act):
     want = a + BO.rows(res)
     s = act_slack(act, p, slack) + 2.0 ** -24 * np.abs(want)
     close(y, BO.heads(want, yh), BO.heads(s, yh), "y")
+    # without a workspace the K blocks are not split
+    yw = torch.empty_like(y)
+    a = vsa._LinearArgs(B=B, x_heads=xh, C=C, y_heads=yh, O=Ow, N=N, act=vsa.ACTS[act])
+    a.x, a.y, a.w = vsa._view(plan, x, "x", x.shape), vsa._view(plan, yw, "y", y.shape), w.data_ptr()
+    a.bias, a.bias_type = vsa._vector(plan, bias, "bias", Ow)
+    a.residual = vsa._view(plan, res, "residual", res.shape)
+    assert vsa.lib().vsa_linear(plan.handle, ctypes.byref(a), None, 0, vsa._stream(None)) == 0
+    close(yw, BO.heads(want, yh), BO.heads(s, yh), "no workspace")
     # without bias and residual; the residual read from y itself
     y2 = vsa.vsa_linear(plan, x, w, act=act, y_heads=yh)
     p2 = BO.linear(x, w)
@@ -394,6 +403,8 @@ def test_linear_refusals():
     refused(2, vsa.vsa_linear, plan, torch.zeros(1, 2, 9, 32, **bf), w)        # heads of 32
     refused(1, vsa.vsa_linear, plan, x, torch.zeros(64, 64, **bf), y=x)        # y over x
     refused(1, vsa.vsa_linear, plan, x[:, :1].expand(1, 9, 64), w)             # broadcast rows
+    wide, tall = torch.zeros(128, 4096, **bf), torch.zeros(1, 40, 4096, **bf)
+    refused(4, vsa.vsa_linear, plan, tall, wide, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     refused(4, vsa.vsa_linear_backward, plan, torch.zeros(1, 9, 128, **bf), x, w,
             ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     refused(1, vsa.vsa_linear_backward, plan, torch.zeros(1, 9, 128, **bf), x, w, dx=x)
@@ -406,7 +417,7 @@ def test_linear_refusals():
         vsa.vsa_linear_backward(plan, torch.zeros(1, 9, 128, **bf), x, w, x_act="silu")
     # plain C: unknown codes
     a = vsa._LinearArgs(B=1, C=64, O=128, N=9, act=7)
-    assert vsa.lib().vsa_linear(plan.handle, ctypes.byref(a), None) == 1
+    assert vsa.lib().vsa_linear(plan.handle, ctypes.byref(a), None, 0, None) == 1
     a = vsa._LinearArgs(B=1, C=64, O=128, N=9, bias_type=2)
-    assert vsa.lib().vsa_linear(plan.handle, ctypes.byref(a), None) == 1
+    assert vsa.lib().vsa_linear(plan.handle, ctypes.byref(a), None, 0, None) == 1
     vsa.vsa_sync_status(plan)

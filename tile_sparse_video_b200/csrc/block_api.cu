@@ -447,7 +447,16 @@ vsa_status vsa_norm_rope_backward(vsa_plan p, vsa_rope rope, const vsa_head_grad
   return launch_norm_rope_backward(p, rope, t, n, eps, tiled == 1, B, H, D, ws, st);
 }
 
-vsa_status vsa_linear(vsa_plan p, const vsa_linear_args* q, void* stream) {
+vsa_status vsa_linear_workspace_size(vsa_plan p, int B, int64_t N, int C, int O, size_t* bytes) {
+  if (p == nullptr || bytes == nullptr) return fail(VSA_ERR_INVALID_ARG, "plan or bytes is NULL");
+  VSA_TRY(check_rows(B, N));
+  VSA_TRY(check_width(0, C, "C"));
+  VSA_TRY(check_width(0, O, "O"));
+  *bytes = linear_bytes(p, B, N, C, O);
+  return VSA_OK;
+}
+
+vsa_status vsa_linear(vsa_plan p, const vsa_linear_args* q, void* ws, size_t ws_bytes, void* stream) {
   VSA_NVTX_RANGE();
   VSA_TRY(check_device(p));
   if (q == nullptr) return fail(VSA_ERR_INVALID_ARG, "args is NULL");
@@ -474,7 +483,12 @@ vsa_status vsa_linear(vsa_plan p, const vsa_linear_args* q, void* stream) {
         q->pre.ptr == q->residual.ptr)
       return fail(VSA_ERR_INVALID_ARG, "pre must not overlap another tensor");
   }
-  return launch_linear(p, *q, static_cast<cudaStream_t>(stream));
+  if (ws != nullptr) {
+    VSA_TRY(check_ptr(ws, "ws"));
+    if (ws_bytes < linear_bytes(p, q->B, q->N, q->C, q->O))
+      return fail(VSA_ERR_WORKSPACE, "workspace too small (see vsa_linear_workspace_size)");
+  }
+  return launch_linear(p, *q, ws, static_cast<cudaStream_t>(stream));
 }
 
 vsa_status vsa_linear_backward_workspace_size(vsa_plan p, int B, int64_t N, int C, int O,
@@ -515,7 +529,7 @@ vsa_status vsa_linear_backward(vsa_plan p, const vsa_linear_grad_args* q, void* 
       if (q->dw == q->dy.ptr || q->dw == q->x.ptr || q->dw == q->w || q->dw == q->dx.ptr)
         return fail(VSA_ERR_INVALID_ARG, "dw must not overlap another tensor");
     }
-    if (q->dw != nullptr || q->db != nullptr) {
+    if (q->dx.ptr != nullptr || q->dw != nullptr || q->db != nullptr) {
       if (ws == nullptr || ws_bytes < linear_backward_bytes(p, q->B, q->N, q->C, q->O))
         return fail(VSA_ERR_WORKSPACE,
                     "workspace missing or too small (see vsa_linear_backward_workspace_size)");

@@ -56,7 +56,9 @@ vsa_status launch_norm_rope_backward(const vsa_plan_s* p, const vsa_rope_s* rope
                                      const HeadGradArgs* t, int n, float eps, bool tiled, int B,
                                      int H, int D, void* ws, cudaStream_t stream);
 
-vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& a, cudaStream_t stream);
+// ws: linear_bytes of it, or NULL (the K blocks are then not split).
+size_t linear_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O);
+vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& a, void* ws, cudaStream_t stream);
 size_t linear_backward_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O);
 vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_args& a, void* ws,
                                   cudaStream_t stream);

@@ -88,7 +88,7 @@ struct GemmArgs {
   OutView y, res, pre;
   const void* bias;
   int bias_f32, act;
-  float* partial;                  // wgrad with splits > 1: fp32 [splits][M][cols]
+  float* partial;                  // with splits > 1: fp32 [splits][M][cols]
 };
 
 // The barrier may be the other CTA's.
@@ -518,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (t + pairs < tiles) read_bias(t + pairs);
       }
-      const bool with_res = kOrder != kWgrad && a.res.ptr != nullptr;
+      const bool with_res = kOrder != kWgrad && a.res.ptr != nullptr && a.splits == 1;
       const bool with_pre = kOrder == kForward && a.pre.ptr != nullptr;
       // nothing of the warp's rows and columns is over the edge
       const bool inside = __all_sync(0xFFFFFFFFu, live == 15u) && col_w + half <= a.cols;
@@ -567,7 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       uint32_t v[32];
       tmem_ld32(acc, v);
-      if (kOrder == kWgrad && a.splits > 1) {
+      if (a.splits > 1) {
         // fp32 partial products, 16 columns (64 bytes) at a time
         for (int c = 0; c < chunks; ++c) {
           tmem_wait_ld(v);
@@ -583,7 +583,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 if (live >> i & 1)
-                  *reinterpret_cast<uint4*>(a.partial + (int64_t(sp) * a.M + tok[i]) * a.cols + col) =
+                  *reinterpret_cast<uint4*>(
+                      a.partial + (int64_t(sp) * a.M + bat[i] * a.Nrow + tok[i]) * a.cols + col) =
                       *chunk_at(st, 8 * i + (lane >> 2), q);
             }
             __syncwarp();
@@ -660,49 +661,193 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// dw = bf16(sum over splits of the fp32 partial products), in split order.
-__global__ void __launch_bounds__(256) split_sum_kernel(const float4* __restrict__ partial,
-                                                        uint2* __restrict__ out, int64_t n4,
-                                                        int splits) {
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n4; i += int64_t(gridDim.x) * 256) {
-    float4 s = partial[i];
-    for (int k = 1; k < splits; ++k) {
-      const float4 v = partial[int64_t(k) * n4 + i];
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
+// ---------------------------------------------------------------- few rows
+// Forward for up to eight rows, where reading w is all there is (2 O C bytes; 8.8 us at the copy
+// rate for 5,376 x 5,376) and tiles of 256 rows would leave most SMs without work.
+// A block takes eight rows of w; its warps share out C.  A lane reads 16 bytes along C of a row
+// of w and of a row of x straight into the fragments of mma.m16n8k16 (x in the first
+// eight of 16 rows): the order of C within 32 columns does not matter to a sum, so lane t's eight
+// neighbours stand for the pairs 2t, 2t + 1, 2t + 8, 2t + 9 of two products.  The warps'
+// fp32 sums meet in shared memory, in warp order.
+constexpr int kFewThreads = 256, kFewUnroll = 7, kFewRows = 8;
+
+struct FewArgs {
+  const uint16_t *x, *w;
+  int64_t xb, xh, xn;
+  int x_shift;                     // column >> x_shift is the head of x
+  int M, N, C, O;
+  OutView y, res, pre;
+  const void* bias;
+  int bias_f32, act;
+};
+
+// d += a b for the first eight rows of a.
+__device__ __forceinline__ void mma_8x8(float (&d)[2], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  float d2 = 0.0f, d3 = 0.0f;
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+      " {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d2), "+f"(d3)
+      : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 load_or_zero(const uint16_t* p, bool live) {
+  return live ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// The epilogue of two neighbouring columns of row r.
+__device__ __forceinline__ void finish(const FewArgs& a, int r, int o, float2 (&f)[1]) {
+  if (a.bias != nullptr) {
+    const float* bf = static_cast<const float*>(a.bias) + o;
+    const uint16_t* bh = static_cast<const uint16_t*>(a.bias) + o;
+    f[0].x += a.bias_f32 ? bf[0] : __uint_as_float(uint32_t(bh[0]) << 16);
+    f[0].y += a.bias_f32 ? bf[1] : __uint_as_float(uint32_t(bh[1]) << 16);
+  }
+  const int b = r / a.N;
+  const int64_t n = r - b * a.N;
+  const auto at = [&](const OutView& v) {
+    return reinterpret_cast<uint32_t*>(v.ptr + b * v.sb + n * v.sn + col_offset(v, o));
+  };
+  if (a.pre.ptr != nullptr) *at(a.pre) = pack_bf16(f[0].x, f[0].y);
+  act_run(a.act, f);
+  if (a.res.ptr != nullptr) {
+    const uint32_t w = *at(a.res);
+    f[0] = add2(f[0], make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)));
+  }
+  *at(a.y) = pack_bf16(f[0].x, f[0].y);
+}
+
+// A piece of w, read once: volatile, so that the loads of a step stay ahead of its products.
+__device__ __forceinline__ uint4 load_w(const uint16_t* p, bool live) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (live)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+  return v;
+}
+
+__global__ void __launch_bounds__(kFewThreads) linear_few_kernel(const __grid_constant__ FewArgs a) {
+  constexpr int kWarps = kFewThreads / 32, kStep = kWarps * 32;
+  __shared__ float sum[kWarps][8][8 + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int o0 = blockIdx.x * 8;                    // O is a multiple of 8
+  const uint16_t* w = a.w + int64_t(o0 + g) * a.C;
+  const int bx = g / a.N;
+  const bool live = g < a.M;
+  const uint16_t* x = a.x + bx * a.xb + int64_t(g - bx * a.N) * a.xn;
+  float acc[2] = {0.0f, 0.0f};
+  for (int k0 = warp * 32 + 8 * t; k0 - 8 * t < a.C; k0 += kStep * kFewUnroll) {
+    uint4 u[kFewUnroll], v[kFewUnroll];
+#pragma unroll
+    for (int i = 0; i < kFewUnroll; ++i) u[i] = load_w(w + k0 + i * kStep, k0 + i * kStep < a.C);
+#pragma unroll
+    for (int i = 0; i < kFewUnroll; ++i) {
+      const int k = k0 + i * kStep, h = k >> a.x_shift;
+      v[i] = load_or_zero(x + h * a.xh + (k - (h << a.x_shift)), live && k < a.C);
     }
-    out[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+#pragma unroll
+    for (int i = 0; i < kFewUnroll; ++i) {
+      mma_8x8(acc, v[i].x, v[i].y, u[i].x, u[i].y);
+      mma_8x8(acc, v[i].z, v[i].w, u[i].z, u[i].w);
+    }
+  }
+  // row g of x, columns 2t and 2t + 1
+  sum[warp][g][2 * t] = acc[0];
+  sum[warp][g][2 * t + 1] = acc[1];
+  __syncthreads();
+  // a thread for two neighbouring columns of a row
+  if (threadIdx.x >= 32) return;
+  const int c = 2 * t, r = g, o = o0 + c;
+  if (r >= a.M) return;
+  float2 f[1] = {make_float2(0.0f, 0.0f)};
+#pragma unroll
+  for (int v = 0; v < kWarps; ++v) f[0] = add2(f[0], make_float2(sum[v][r][c], sum[v][r][c + 1]));
+  finish(a, r, o, f);
+}
+
+// The join of split products: partials are summed in split order, and what the tiles'
+// epilogue would have done follows.  A thread takes eight columns of a row.
+template <int kOrder>
+__global__ void __launch_bounds__(256) split_join_kernel(const __grid_constant__ GemmArgs a, const Div by_oct) {
+  const uint32_t total = uint32_t(a.M) * by_oct.d;
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+    const uint32_t r = i / by_oct;
+    const int col = int(i - r * by_oct.d) * 8;
+    float2 f[4] = {};
+    const float* p = a.partial + int64_t(r) * a.cols + col;
+    for (int k = 0; k < a.splits; ++k, p += a.M * a.cols) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(p)), v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      f[0] = add2(f[0], make_float2(u.x, u.y));
+      f[1] = add2(f[1], make_float2(u.z, u.w));
+      f[2] = add2(f[2], make_float2(v.x, v.y));
+      f[3] = add2(f[3], make_float2(v.z, v.w));
+    }
+    const uint32_t b = r / a.by_nrow;
+    const int64_t n = r - b * a.by_nrow.d;
+    const auto at = [&](const OutView& v) {
+      return reinterpret_cast<uint4*>(v.ptr + b * v.sb + n * v.sn + col_offset(v, col));
+    };
+    if (kOrder == kForward) {
+      if (a.bias != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float* bf = static_cast<const float*>(a.bias) + col + 2 * e;
+          const uint16_t* bh = static_cast<const uint16_t*>(a.bias) + col + 2 * e;
+          f[e] = add2(f[e], a.bias_f32 ? make_float2(bf[0], bf[1])
+                                       : make_float2(__uint_as_float(uint32_t(bh[0]) << 16),
+                                                     __uint_as_float(uint32_t(bh[1]) << 16)));
+        }
+      }
+      if (a.pre.ptr != nullptr) *at(a.pre) = pack(f);
+      act_run(a.act, f);
+    }
+    if (kOrder != kWgrad && a.res.ptr != nullptr) {
+      float2 x[4];
+      unpack(*at(a.res), x);
+      if (kOrder == kForward) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = add2(f[e], x[e]);
+      } else {
+        slope_run(a.act, x, f);
+      }
+    }
+    *at(a.y) = pack(f);
   }
 }
 
 // Column sums of dy [B, heads, N, D] -> fp32 [O]: a block takes 256 columns (32 lanes of 8) of a
-// run of rows, 8 warps side by side; part[blockIdx.y][O], summed by colsum_join_kernel.
-__global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, int64_t Nrow, int64_t M,
-                                                     int O, int64_t rows_per, float* part) {
+// run of rows, 8 warps side by side with 8 rows each in flight; part[blockIdx.y][O], summed in
+// order by colsum_join_kernel.
+constexpr int kColsumRows = 64;
+
+__global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, const Div by_nrow, int M, int O,
+                                                     int rows_per, float* part) {
   __shared__ float s[8][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 256 + 8 * lane;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const int64_t r0 = int64_t(blockIdx.y) * rows_per, r1 = min(M, r0 + rows_per);
+  float2 acc[4] = {};
+  const int r0 = blockIdx.y * rows_per, r1 = min(M, r0 + rows_per);
   if (col < O) {
-#pragma unroll 4
-    for (int64_t r = r0 + warp; r < r1; r += 8) {
-      const int64_t b = r / Nrow;
-      const uint4 v = *reinterpret_cast<const uint4*>(dy.ptr + b * dy.sb + (r - b * Nrow) * dy.sn +
-                                                      col_offset(dy, col));
-      float2 f[4];
-      unpack(v, f);
+    const uint16_t* base = dy.ptr + col_offset(dy, col);
+    for (int r = r0 + warp; r < r1; r += kColsumRows) {
+      uint4 v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[2 * e] += f[e].x;
-        acc[2 * e + 1] += f[e].y;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t ri = r + 8 * i, b = ri / by_nrow;
+        v[i] = load_or_zero(base + b * dy.sb + (ri - b * by_nrow.d) * dy.sn, int(ri) < r1);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float2 f[4];
+        unpack(v[i], f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = add2(acc[e], f[e]);
       }
     }
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s[warp][8 * lane + e] = acc[e];
+  for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(&s[warp][8 * lane + 2 * e]) = acc[e];
   __syncthreads();
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c < O) {
@@ -713,20 +858,21 @@ __global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, int64_t N
   }
 }
 
-__global__ void __launch_bounds__(256) colsum_join_kernel(const float* part, int runs, int O,
-                                                          float* db) {
-  __shared__ float s[8][33];
+__global__ void __launch_bounds__(1024) colsum_join_kernel(const float* part, int runs, int O, float* db) {
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < O)
-    for (int i = warp; i < runs; i += 8) v += part[int64_t(i) * O + c];
+  if (c < O) {
+#pragma unroll 8
+    for (int i = warp; i < runs; i += 32) v += part[int64_t(i) * O + c];
+  }
   s[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && c < O) {
     float t = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += s[w][lane];
+    for (int w = 0; w < 32; ++w) t += s[w][lane];
     db[c] = t;
   }
 }
@@ -801,31 +947,53 @@ int sms(const vsa_plan_s* p) { return p->num_sms > 0 ? p->num_sms : 148; }
 
 int pairs_of(const vsa_plan_s* p) { return sms(p) / 2; }
 
-// Columns of a tile: 256, or 128 where that shortens the waves of tiles over the pairs of SMs.  A
-// tile of 128 columns takes 0.72 of the time of one of 256 (20 of 29 us at K = 5,376, 4.8 of
-// 6.5 us at K = 1,024): its products want half as much again of operand bytes a cycle.
-int tile_columns(const vsa_plan_s* p, int64_t m_tiles, int cols) {
-  const int64_t n = pairs_of(p);
-  const int64_t t256 = m_tiles * ((cols + 255) / 256), t128 = m_tiles * ((cols + 127) / 128);
-  return (t128 + n - 1) / n * 18 < (t256 + n - 1) / n * 25 ? 128 : 256;
+// Columns of a tile (256 or 128) and splits of the K blocks, by the time they should take, in us:
+// a wave of tiles over the pairs of SMs takes 0.35 a K block with 256 columns and 0.25 with 128
+// (measured: 29 and 20 us at K = 5,376; a tile of 128 columns wants half as much again of operand
+// bytes a product), and 2.5 for its start and end; a split costs the join, a launch and two
+// passes over its fp32 partial sums at some 4 TB/s.
+struct Tiling {
+  int bn, splits;
+};
+Tiling tiling(const vsa_plan_s* p, int64_t m_tiles, int64_t M, int cols, int k_blocks, bool may_split) {
+  Tiling best = {256, 1};
+  double least = 1e300;
+  for (const int bn : {256, 128})
+    for (int s = 1; s <= (may_split ? std::min(16, k_blocks / 4) : 1) || s == 1; ++s) {
+      const int64_t tiles = m_tiles * ((cols + bn - 1) / bn) * s;
+      const int64_t waves = (tiles + pairs_of(p) - 1) / pairs_of(p);
+      if (s > 1 && waves > 1) break;
+      const double join = s > 1 ? 3.0 + double(s) * double(M) * cols * 8 / 4e6 : 0.0;
+      const double t = double(waves) * (((k_blocks + s - 1) / s) * (bn == 256 ? 0.35 : 0.25) + 2.5) + join;
+      if (t < least) {
+        least = t;
+        best = {bn, s};
+      }
+    }
+  return best;
+}
+// fp32 partial products of `splits`, in bytes.
+size_t split_bytes(int splits, int64_t M, int cols) {
+  return splits > 1 ? (size_t(splits) * size_t(M) * size_t(cols) * sizeof(float) + 15) / 16 * 16 : 0;
 }
 
-// Splits of the rows of a weight gradient: as many as leave every pair of SMs a tile of at
-// least 8 K blocks.
-int wgrad_splits(const vsa_plan_s* p, int O, int C, int k_blocks) {
-  const int64_t m_tiles = (O + kBM - 1) / kBM;
-  const int bn = tile_columns(p, m_tiles, C);
-  const int64_t tiles = m_tiles * ((C + bn - 1) / bn);
-  return int(std::max<int64_t>(1, std::min<int64_t>(pairs_of(p) / tiles, k_blocks / 8)));
+// Tiles of the output and splits of the K blocks, evenly; no split is left without one.
+void set_tiles(const vsa_plan_s* p, GemmArgs* a, bool may_split) {
+  const Tiling t = tiling(p, a->m_tiles, a->M, a->cols, a->k_blocks, may_split);
+  a->bn = t.bn;
+  a->n_tiles = (a->cols + t.bn - 1) / t.bn;
+  a->k_split = (a->k_blocks + t.splits - 1) / t.splits;
+  a->splits = (a->k_blocks + a->k_split - 1) / a->k_split;
 }
 
 int row_blocks(const View& v, int rows) { return int((v.N + rows - 1) / rows); }
 
-constexpr int64_t kColsumRows = 256;      // rows of a column-sum block, at least
-
-int colsum_runs(int64_t M) {
-  return int(std::max<int64_t>(1, std::min<int64_t>(256, (M + kColsumRows - 1) / kColsumRows)));
+// Runs of rows of the column sums: 64 rows each, more where that made more than 512 runs.
+int colsum_rows(int64_t M) {
+  const int64_t per = (M + 511) / 512;
+  return int(std::max<int64_t>(1, (per + kColsumRows - 1) / kColsumRows) * kColsumRows);
 }
+int colsum_runs(int64_t M) { return int(std::max<int64_t>(1, (M + colsum_rows(M) - 1) / colsum_rows(M))); }
 
 template <int kOrder>
 vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv, int b_box,
@@ -850,27 +1018,66 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
   const int grid = 2 * int(std::min<int64_t>(tiles, pairs_of(p)));
   linear_kernel<kOrder><<<grid, kThreads, kSmem, stream>>>(ma, mb, a);
   e = cudaGetLastError();
+  if (e == cudaSuccess && a.splits > 1) {
+    const int64_t octets = a.M * (a.cols / 8);
+    const int blocks = int(std::min<int64_t>((octets + 255) / 256, int64_t(sms(p)) * 8));
+    split_join_kernel<kOrder><<<blocks, 256, 0, stream>>>(a, make_div(a.cols / 8));
+    e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? VSA_OK
+                          : fail(VSA_ERR_CUDA, std::string("linear launch: ") + cudaGetErrorString(e));
+}
+
+vsa_status launch_few(const vsa_linear_args& q, cudaStream_t stream) {
+  FewArgs a = {};
+  const View x = make_view(q.x, q.B, q.N, q.x_heads, q.C);
+  a.x = x.ptr;
+  a.w = static_cast<const uint16_t*>(q.w);
+  a.xb = x.sb;
+  a.xh = x.H > 1 ? x.sh : 0;
+  a.xn = x.sn;
+  a.x_shift = q.x_heads > 0 ? (x.D == 64 ? 6 : 7) : 31;
+  a.M = int(q.B * q.N);
+  a.N = int(q.N);
+  a.C = q.C;
+  a.O = q.O;
+  a.y = out_view(q.y, q.y_heads, q.O);
+  a.res = out_view(q.residual, q.y_heads, q.O);
+  a.pre = out_view(q.pre, q.y_heads, q.O);
+  a.bias = q.bias;
+  a.bias_f32 = q.bias_type == VSA_F32;
+  a.act = q.act;
+  linear_few_kernel<<<q.O / 8, kFewThreads, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VSA_OK
                           : fail(VSA_ERR_CUDA, std::string("linear launch: ") + cudaGetErrorString(e));
 }
 
 }  // namespace
 
-vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, cudaStream_t stream) {
+size_t linear_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
+  const int64_t M = int64_t(B) * N;
+  if (M <= kFewRows) return 0;
+  // tiles and K blocks of either flattening, rows or heads
+  const int64_t m1 = (M + kBM - 1) / kBM, m2 = int64_t(B) * ((N + kBM - 1) / kBM);
+  const int kb = (C + kBK - 1) / kBK;
+  return split_bytes(std::max(tiling(p, m1, M, O, kb, true).splits, tiling(p, m2, M, O, kb, true).splits), M, O);
+}
+
+vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, void* ws, cudaStream_t stream) {
+  if (int64_t(q.B) * q.N <= kFewRows) return launch_few(q, stream);
   View x = make_view(q.x, q.B, q.N, q.x_heads, q.C);
   if (rows_even(x)) flatten(&x);
   GemmArgs a = {};
   a.rows_b = row_blocks(x, kBM);
   a.m_tiles = int(x.B) * a.rows_b;
-  a.bn = tile_columns(p, a.m_tiles, q.O);
-  a.n_tiles = (q.O + a.bn - 1) / a.bn;
   a.ac = cols_of(x);
   a.k_blocks = x.H * a.ac.blocks;
-  a.k_split = a.k_blocks;
-  a.splits = 1;
   a.N = x.N;
   a.M = x.B * x.N;
   a.cols = q.O;
+  set_tiles(p, &a, ws != nullptr);
+  a.partial = static_cast<float*>(ws);
   a.Nrow = q.N;
   a.y = out_view(q.y, q.y_heads, q.O);
   a.res = out_view(q.residual, q.y_heads, q.O);
@@ -882,13 +1089,17 @@ vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, cudaStre
 }
 
 size_t linear_backward_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
-  // the K blocks of either flattening
+  // one buffer, used in turn by the products' partial sums and the column sums; tiles and K blocks of
+  // either flattening, rows or heads
   const int64_t M = int64_t(B) * N;
-  const int64_t kb = std::max((M + kBK - 1) / kBK, int64_t(B) * ((N + kBK - 1) / kBK));
-  const int s = wgrad_splits(p, O, C, int(std::min<int64_t>(kb, 1 << 30)));
-  const size_t split = s > 1 ? size_t(s) * O * C * sizeof(float) : 0;
-  const size_t sums = size_t(colsum_runs(M)) * O * sizeof(float);
-  return (split + 15) / 16 * 16 + sums;
+  const int64_t m1 = (M + kBM - 1) / kBM, m2 = int64_t(B) * ((N + kBM - 1) / kBM);
+  const int64_t k1 = (M + kBK - 1) / kBK, k2 = int64_t(B) * ((N + kBK - 1) / kBK);
+  const int ko = (O + kBK - 1) / kBK;
+  const int64_t mo = (O + kBM - 1) / kBM;
+  const int dgrad = std::max(tiling(p, m1, M, C, ko, true).splits, tiling(p, m2, M, C, ko, true).splits);
+  const int wgrad = std::max(tiling(p, mo, O, C, int(k1), true).splits, tiling(p, mo, O, C, int(k2), true).splits);
+  return std::max({split_bytes(dgrad, M, C), split_bytes(wgrad, O, C),
+                   size_t(colsum_runs(M)) * O * sizeof(float)});
 }
 
 vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_args& q, void* ws,
@@ -907,15 +1118,13 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     GemmArgs a = {};
     a.rows_b = row_blocks(g, kBM);
     a.m_tiles = int(g.B) * a.rows_b;
-    a.bn = tile_columns(p, a.m_tiles, q.C);
-    a.n_tiles = (q.C + a.bn - 1) / a.bn;
     a.ac = cols_of(g);
     a.k_blocks = g.H * a.ac.blocks;
-    a.k_split = a.k_blocks;
-    a.splits = 1;
     a.N = g.N;
     a.M = M;
     a.cols = q.C;
+    set_tiles(p, &a, true);
+    a.partial = static_cast<float*>(ws);
     a.Nrow = q.N;
     a.y = out_view(q.dx, q.x_heads, q.C);
     a.res = out_view(q.x_pre, q.x_heads, q.C);
@@ -924,7 +1133,6 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
                                          int64_t(q.O) * q.C * 2, stream);
     if (st != VSA_OK) return st;
   }
-  float* sums = static_cast<float*>(ws);
   if (q.dw != nullptr) {
     View g = dy, x = make_view(q.x, q.B, q.N, q.x_heads, q.C);
     if (rows_even(g) && rows_even(x)) {
@@ -934,39 +1142,26 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     GemmArgs a = {};
     a.rows_b = row_blocks(g, kBK);
     a.k_blocks = int(g.B) * a.rows_b;
-    a.splits = wgrad_splits(p, q.O, q.C, a.k_blocks);
-    a.k_split = (a.k_blocks + a.splits - 1) / a.splits;
-    a.splits = (a.k_blocks + a.k_split - 1) / a.k_split;
     a.m_tiles = (q.O + kBM - 1) / kBM;
-    a.bn = tile_columns(p, a.m_tiles, q.C);
-    a.n_tiles = (q.C + a.bn - 1) / a.bn;
     a.ac = cols_of(g);
     a.bc = cols_of(x);
     a.N = g.N;
     a.M = q.O;
     a.cols = q.C;
+    set_tiles(p, &a, true);
     a.Nrow = q.O;
     a.y = OutView{static_cast<uint16_t*>(q.dw), 0, 0, q.C, 31};
     a.partial = static_cast<float*>(ws);
     // the rows are long: all column tiles of one group share the pass over them
     const vsa_status st = launch<kWgrad>(p, g, kBK, x, kBK, a, 0, stream);
     if (st != VSA_OK) return st;
-    if (a.splits > 1) {
-      const int64_t n4 = int64_t(q.O) * q.C / 4;
-      const int blocks = int(std::min<int64_t>((n4 + 255) / 256, int64_t(sms(p)) * 8));
-      split_sum_kernel<<<blocks, 256, 0, stream>>>(static_cast<const float4*>(ws),
-                                                   static_cast<uint2*>(q.dw), n4, a.splits);
-      const cudaError_t e = cudaGetLastError();
-      if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
-      sums += (int64_t(a.splits) * q.O * q.C + 3) / 4 * 4;
-    }
   }
   if (q.db != nullptr) {
     const int runs = colsum_runs(M);
-    const int64_t rows_per = (M + runs - 1) / runs;
+    float* sums = static_cast<float*>(ws);
     colsum_kernel<<<dim3((q.O + 255) / 256, runs), 256, 0, stream>>>(
-        out_view(q.dy, q.y_heads, q.O), q.N, M, q.O, rows_per, sums);
-    colsum_join_kernel<<<(q.O + 31) / 32, 256, 0, stream>>>(sums, runs, q.O, q.db);
+        out_view(q.dy, q.y_heads, q.O), make_div(q.N), int(M), q.O, colsum_rows(M), sums);
+    colsum_join_kernel<<<(q.O + 31) / 32, 1024, 0, stream>>>(sums, runs, q.O, q.db);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
   }

@@ -38,7 +38,8 @@ EXPORTS = ("vsa_plan_create", "vsa_plan_info", "vsa_plan_tables", "vsa_keep_coun
 # those of include/vsa_block.h
 BLOCK_EXPORTS = ("vsa_rope_create", "vsa_rope_tables", "vsa_rope_destroy", "vsa_rope_apply",
                  "vsa_norm_rope", "vsa_norm_rope_permute_pool",
-                 "vsa_norm_rope_backward_workspace_size", "vsa_norm_rope_backward", "vsa_linear",
+                 "vsa_norm_rope_backward_workspace_size", "vsa_norm_rope_backward",
+                 "vsa_linear_workspace_size", "vsa_linear",
                  "vsa_linear_backward_workspace_size", "vsa_linear_backward", "vsa_act_backward")
 
 ACTS = {"identity": 0, "sigmoid": 1, "gelu_tanh": 2, "silu": 3}
@@ -147,7 +148,8 @@ def lib():
             "vsa_norm_rope_permute_pool": [P, P, ctypes.POINTER(_HeadTensor), I, F, I, I, I, V],
             "vsa_norm_rope_backward_workspace_size": [P, I, I, ctypes.POINTER(Z)],
             "vsa_norm_rope_backward": [P, P, ctypes.POINTER(_HeadGrad), I, F, I, I, I, I, V, Z, V],
-            "vsa_linear": [P, ctypes.POINTER(_LinearArgs), V],
+            "vsa_linear_workspace_size": [P, I, I64, I, I, ctypes.POINTER(Z)],
+            "vsa_linear": [P, ctypes.POINTER(_LinearArgs), V, Z, V],
             "vsa_linear_backward_workspace_size": [P, I, I64, I, I, ctypes.POINTER(Z)],
             "vsa_linear_backward": [P, ctypes.POINTER(_LinearGradArgs), V, Z, V],
             "vsa_act_backward": [P, V, V, I, V, I64, V],
@@ -878,14 +880,21 @@ def _sides(t: torch.Tensor, name: str):
     return B, N, 0, C
 
 
+def _linear_bytes(plan: Plan, B: int, N: int, C: int, O: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().vsa_linear_workspace_size(plan.handle, B, N, C, O, ctypes.byref(b)))
+    return b.value
+
+
 def vsa_linear(plan: Plan, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
                act: str = "identity", residual: Optional[torch.Tensor] = None, y_heads: int = 0,
                y: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
-               stream=None) -> torch.Tensor:
+               ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = residual + act(x w^T + bias), one kernel.  x: rows [B,N,C] or heads
     [B,H,N,D] (C = H*D), any strides; w [O,C]; bias [O] bf16 or fp32.  y: rows, or
     heads where ``y_heads`` (or the given y, residual) says so.  ``pre`` receives
-    x w^T + bias (what the activation's backward reads).  ``residual`` may be y."""
+    x w^T + bias (what the activation's backward reads).  ``residual`` may be y.
+    ``ws``: workspace (None: allocated where vsa_linear_workspace_size asks for one)."""
     B, N, xh, C = _sides(x, "x")
     O = w.shape[0]
     like = y if y is not None else residual if residual is not None else pre
@@ -902,7 +911,11 @@ def vsa_linear(plan: Plan, x: torch.Tensor, w: torch.Tensor, bias: Optional[torc
     if y is None:
         y = _Out(plan, stream)(shape)
     a.y = _view(plan, y, "y", shape)
-    _check(lib().vsa_linear(plan.handle, ctypes.byref(a), _stream(stream)))
+    if ws is None:
+        n = _linear_bytes(plan, B, N, C, O)
+        ws = _Out(plan, stream)((n,), torch.uint8) if n else None
+    _check(lib().vsa_linear(plan.handle, ctypes.byref(a), _ptr(ws),
+                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
     return y
 
 
