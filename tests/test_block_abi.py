@@ -109,6 +109,10 @@ def test_host_only_plan_refuses_launches(libvsa):
     assert L.vsa_linear_workspace_size(plan.handle, 1, 1, 4096, 256, ctypes.byref(n)) == 0 and n.value == 0
     assert L.vsa_linear_workspace_size(plan.handle, 1, 64, 4096, 256, ctypes.byref(n)) == 0
     assert n.value > 0 and n.value % (64 * 256 * 4) == 0
+    for B, N in ((0, 5), (2, 0), (0, 0)):                 # no rows, no workspace
+        assert L.vsa_linear_workspace_size(plan.handle, B, N, 64, 64, ctypes.byref(n)) == 0 and n.value == 0
+        assert L.vsa_linear_backward_workspace_size(plan.handle, B, N, 64, 64, ctypes.byref(n)) == 0
+        assert n.value == 0
     # the handle does not refer to its plan
     plan.close()
     assert rope.tables()[0].shape == (366, 32)

@@ -77,7 +77,8 @@ struct GemmArgs {
   int m_tiles, n_tiles, group;     // output tiles and the column group of the order
   Div by_group, by_width, by_last; // tiles of a group; its columns, and the last group's
   Div by_splits, by_rows_b, by_nrow;
-  int k_blocks, k_split, splits;   // K blocks, and how many one split takes
+  // whole tiles come first, in full waves; the rest are split along K, k_split blocks each
+  int k_blocks, k_split, splits, whole;
   int rows_b;                      // row blocks (tiles, or K blocks in wgrad) per batch element
   int64_t N;                       // rows of a batch element of the TMA views
   int64_t M;                       // valid rows of the output (rows of dw in wgrad)
@@ -88,7 +89,7 @@ struct GemmArgs {
   OutView y, res, pre;
   const void* bias;
   int bias_f32, act;
-  float* partial;                  // with splits > 1: fp32 [splits][M][cols]
+  float* partial;                  // fp32 [splits][tiles - whole][256][bn]
 };
 
 // The barrier may be the other CTA's.
@@ -154,15 +155,22 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       : "memory");
 }
 
-// Work item t -> split, and output tile (m, n): the column tiles in groups, m-major within one.
-__device__ __forceinline__ void decode(int t, const GemmArgs& a, int& sp, int& m, int& n) {
-  const uint32_t tile = uint32_t(t) / a.by_splits;
-  sp = t - int(tile) * a.splits;
+// Output tile -> its row and column tile: the column tiles in groups, m-major within one.
+__device__ __forceinline__ void decode(uint32_t tile, const GemmArgs& a, int& m, int& n) {
   const uint32_t g = tile / a.by_group, r = tile - g * a.by_group.d;
   const int first = int(g) * a.group;
   const bool last = first + a.group >= a.n_tiles;
   m = int(last ? r / a.by_last : r / a.by_width);
   n = first + int(r) - m * int(last ? a.by_last.d : a.by_width.d);
+}
+// Work item t: a whole tile, or split sp of one.
+struct Item {
+  int tile, sp, k0, k1;
+};
+__device__ __forceinline__ Item item_of(int t, const GemmArgs& a) {
+  if (t < a.whole) return {t, -1, 0, a.k_blocks};
+  const int u = t - a.whole, i = int(uint32_t(u) / a.by_splits), sp = u - i * a.splits;
+  return {a.whole + i, sp, sp * a.k_split, min(a.k_blocks, (sp + 1) * a.k_split)};
 }
 
 // Two fp32 values at a time: the epilogue's arithmetic is bound by its instructions.
@@ -291,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0);
   const int rank = int(cluster_rank());
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tiles = a.m_tiles * a.n_tiles * a.splits;
+  const int items = a.whole + (a.m_tiles * a.n_tiles - a.whole) * a.splits;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -335,11 +343,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       const int half = a.bn / 2;         // this CTA's columns of the B block
       const uint32_t lead = at_leader(full);
-      for (int t = pair; t < tiles && ok; t += pairs) {
-        int sp, m, n;
-        decode(t, a, sp, m, n);
+      for (int t = pair; t < items && ok; t += pairs) {
+        const Item it = item_of(t, a);
+        int m, n;
+        decode(it.tile, a, m, n);
         const int b0 = n * a.bn + rank * half;
-        const int k0 = sp * a.k_split, k1 = min(a.k_blocks, k0 + a.k_split);
+        const int k0 = it.k0, k1 = it.k1;
         // along K: block `i` of `per` in head (or batch element) `o`
         const int per = kAMn ? a.rows_b : a.ac.blocks;
         int o = k0 / per, i = k0 - o * per;
@@ -415,9 +424,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t s = 0, phase = 0;
       int lt = 0;
       bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
-        const int k0 = (t - int(uint32_t(t) / a.by_splits) * a.splits) * a.k_split;
-        const int nk = min(a.k_blocks, k0 + a.k_split) - k0;
+      for (int t = pair; t < items && ok; t += pairs, ++lt) {
+        const Item it = item_of(t, a);
+        const int nk = it.k1 - it.k0;
         const int buf = lt & 1;
         if (lt >= 2 && !wait_warp(acc_empty + 8 * buf, ((lt >> 1) - 1) & 1, abort_flag, a.status, 32)) {
           ok = false;
@@ -470,8 +479,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int row0 = rank * 128 + quad * 32;         // first row of the warp in the tile
     float next_bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // column 32 i + lane of the next tile
     const auto read_bias = [&](int t) {
-      int sp, m, n;
-      decode(t, a, sp, m, n);
+      int m, n;
+      decode(item_of(t, a).tile, a, m, n);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int col = n * a.bn + side * half + 32 * i + lane;
@@ -482,11 +491,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                          : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.bias) + col)) << 16);
       }
     };
-    if (kOrder == kForward && a.bias != nullptr && pair < tiles) read_bias(pair);
+    if (kOrder == kForward && a.bias != nullptr && pair < items) read_bias(pair);
     int lt = 0;
-    for (int t = pair; t < tiles; t += pairs, ++lt) {
-      int sp, m, n;
-      decode(t, a, sp, m, n);
+    for (int t = pair; t < items; t += pairs, ++lt) {
+      const Item it = item_of(t, a);
+      int m, n;
+      decode(it.tile, a, m, n);
       const int buf = lt & 1;
       const uint32_t acc = tmem + buf * 256 + (uint32_t(quad * 32) << 16) + uint32_t(side * half);
       // four lanes write a row's 64 bytes: this lane's rows are 8 i + lane / 4
@@ -516,9 +526,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) bias[32 * i + lane] = next_bias[i];
         __syncwarp();
-        if (t + pairs < tiles) read_bias(t + pairs);
+        if (t + pairs < items) read_bias(t + pairs);
       }
-      const bool with_res = kOrder != kWgrad && a.res.ptr != nullptr && a.splits == 1;
+      const bool with_res = kOrder != kWgrad && a.res.ptr != nullptr && it.sp < 0;
       const bool with_pre = kOrder == kForward && a.pre.ptr != nullptr;
       // nothing of the warp's rows and columns is over the edge
       const bool inside = __all_sync(0xFFFFFFFFu, live == 15u) && col_w + half <= a.cols;
@@ -567,8 +577,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       uint32_t v[32];
       tmem_ld32(acc, v);
-      if (a.splits > 1) {
-        // fp32 partial products, 16 columns (64 bytes) at a time
+      if (it.sp >= 0) {
+        // fp32 partial products of the tile's rows, 16 columns (64 bytes) at a time
+        float* slot = a.partial + (int64_t(it.sp) * (a.m_tiles * a.n_tiles - a.whole) + it.tile - a.whole) *
+                                      (kBM * a.bn) +
+                      (row0 + (lane >> 2)) * a.bn + side * half + 4 * q;
         for (int c = 0; c < chunks; ++c) {
           tmem_wait_ld(v);
 #pragma unroll
@@ -578,15 +591,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               *chunk_at(st, lane, e) = make_uint4(v[16 * j + 4 * e], v[16 * j + 4 * e + 1],
                                                   v[16 * j + 4 * e + 2], v[16 * j + 4 * e + 3]);
             __syncwarp();
-            const int col = col_w + 32 * c + 16 * j + 4 * q;
-            if (col < a.cols) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (live >> i & 1)
-                  *reinterpret_cast<uint4*>(
-                      a.partial + (int64_t(sp) * a.M + bat[i] * a.Nrow + tok[i]) * a.cols + col) =
-                      *chunk_at(st, 8 * i + (lane >> 2), q);
-            }
+            for (int i = 0; i < 4; ++i)
+              if (live >> i & 1)
+                *reinterpret_cast<uint4*>(slot + 8 * i * a.bn + 32 * c + 16 * j) =
+                    *chunk_at(st, 8 * i + (lane >> 2), q);
             __syncwarp();
           }
           if (c + 1 < chunks) tmem_ld32(acc + 32 * c + 32, v);
@@ -669,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // eight of 16 rows): the order of C within 32 columns does not matter to a sum, so lane t's eight
 // neighbours stand for the pairs 2t, 2t + 1, 2t + 8, 2t + 9 of two products.  The warps'
 // fp32 sums meet in shared memory, in warp order.
-constexpr int kFewThreads = 256, kFewUnroll = 7, kFewRows = 8;
+constexpr int kFewThreads = 256, kFewUnroll = 4, kFewRows = 8;
 
 struct FewArgs {
   const uint16_t *x, *w;
@@ -726,7 +735,7 @@ __device__ __forceinline__ uint4 load_w(const uint16_t* p, bool live) {
   return v;
 }
 
-__global__ void __launch_bounds__(kFewThreads) linear_few_kernel(const __grid_constant__ FewArgs a) {
+__global__ void __launch_bounds__(kFewThreads, 4) linear_few_kernel(const __grid_constant__ FewArgs a) {
   constexpr int kWarps = kFewThreads / 32, kStep = kWarps * 32;
   __shared__ float sum[kWarps][8][8 + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -737,14 +746,18 @@ __global__ void __launch_bounds__(kFewThreads) linear_few_kernel(const __grid_co
   const bool live = g < a.M;
   const uint16_t* x = a.x + bx * a.xb + int64_t(g - bx * a.N) * a.xn;
   float acc[2] = {0.0f, 0.0f};
-  for (int k0 = warp * 32 + 8 * t; k0 - 8 * t < a.C; k0 += kStep * kFewUnroll) {
+  const int first = warp * 32 + 8 * t;
+  uint4 next[kFewUnroll];                            // the step's pieces of w, a step ahead
+#pragma unroll
+  for (int i = 0; i < kFewUnroll; ++i) next[i] = load_w(w + first + i * kStep, first + i * kStep < a.C);
+  for (int k0 = first; k0 - 8 * t < a.C; k0 += kStep * kFewUnroll) {
     uint4 u[kFewUnroll], v[kFewUnroll];
 #pragma unroll
-    for (int i = 0; i < kFewUnroll; ++i) u[i] = load_w(w + k0 + i * kStep, k0 + i * kStep < a.C);
-#pragma unroll
     for (int i = 0; i < kFewUnroll; ++i) {
-      const int k = k0 + i * kStep, h = k >> a.x_shift;
+      const int k = k0 + i * kStep, h = k >> a.x_shift, kn = k + kStep * kFewUnroll;
+      u[i] = next[i];
       v[i] = load_or_zero(x + h * a.xh + (k - (h << a.x_shift)), live && k < a.C);
+      next[i] = load_w(w + kn, kn < a.C);
     }
 #pragma unroll
     for (int i = 0; i < kFewUnroll; ++i) {
@@ -766,54 +779,66 @@ __global__ void __launch_bounds__(kFewThreads) linear_few_kernel(const __grid_co
   finish(a, r, o, f);
 }
 
-// The join of split products: partials are summed in split order, and what the tiles'
-// epilogue would have done follows.  A thread takes eight columns of a row.
+// The join of split tiles: partials are summed in split order, and what the tiles' epilogue
+// would have done follows.  A thread takes eight columns of a row, a block 2,048 elements of a tile.
 template <int kOrder>
-__global__ void __launch_bounds__(256) split_join_kernel(const __grid_constant__ GemmArgs a, const Div by_oct) {
-  const uint32_t total = uint32_t(a.M) * by_oct.d;
-  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
-    const uint32_t r = i / by_oct;
-    const int col = int(i - r * by_oct.d) * 8;
-    float2 f[4] = {};
-    const float* p = a.partial + int64_t(r) * a.cols + col;
-    for (int k = 0; k < a.splits; ++k, p += a.M * a.cols) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(p)), v = __ldg(reinterpret_cast<const float4*>(p) + 1);
-      f[0] = add2(f[0], make_float2(u.x, u.y));
-      f[1] = add2(f[1], make_float2(u.z, u.w));
-      f[2] = add2(f[2], make_float2(v.x, v.y));
-      f[3] = add2(f[3], make_float2(v.z, v.w));
-    }
-    const uint32_t b = r / a.by_nrow;
-    const int64_t n = r - b * a.by_nrow.d;
-    const auto at = [&](const OutView& v) {
-      return reinterpret_cast<uint4*>(v.ptr + b * v.sb + n * v.sn + col_offset(v, col));
-    };
-    if (kOrder == kForward) {
-      if (a.bias != nullptr) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float* bf = static_cast<const float*>(a.bias) + col + 2 * e;
-          const uint16_t* bh = static_cast<const uint16_t*>(a.bias) + col + 2 * e;
-          f[e] = add2(f[e], a.bias_f32 ? make_float2(bf[0], bf[1])
-                                       : make_float2(__uint_as_float(uint32_t(bh[0]) << 16),
-                                                     __uint_as_float(uint32_t(bh[1]) << 16)));
-        }
-      }
-      if (a.pre.ptr != nullptr) *at(a.pre) = pack(f);
-      act_run(a.act, f);
-    }
-    if (kOrder != kWgrad && a.res.ptr != nullptr) {
-      float2 x[4];
-      unpack(*at(a.res), x);
-      if (kOrder == kForward) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = add2(f[e], x[e]);
-      } else {
-        slope_run(a.act, x, f);
-      }
-    }
-    *at(a.y) = pack(f);
+__global__ void __launch_bounds__(256) split_join_kernel(const __grid_constant__ GemmArgs a) {
+  const int octs = a.bn / 8, per_block = 256 / octs;       // rows of a block
+  const int i = blockIdx.x / (kBM / per_block), part = blockIdx.x % (kBM / per_block);
+  const int in_tile = part * per_block + threadIdx.x / octs, in_row = (threadIdx.x % octs) * 8;
+  int m, tn;
+  decode(a.whole + i, a, m, tn);
+  const int col = tn * a.bn + in_row;
+  uint32_t r;                                              // row of the output
+  if (kOrder == kWgrad) {
+    r = uint32_t(m) * kBM + in_tile;
+    if (r >= a.M) return;
+  } else {
+    const uint32_t mb = uint32_t(m) / a.by_rows_b, in_b = (uint32_t(m) - mb * uint32_t(a.rows_b)) * kBM + in_tile;
+    if (in_b >= a.N) return;
+    r = mb * uint32_t(a.N) + in_b;
   }
+  if (col >= a.cols) return;
+  float2 f[4] = {};
+  const float* p = a.partial + int64_t(i) * (kBM * a.bn) + in_tile * a.bn + in_row;
+  const int64_t next = int64_t(a.m_tiles * a.n_tiles - a.whole) * (kBM * a.bn);
+  for (int k = 0; k < a.splits; ++k, p += next) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(p)), v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = add2(f[0], make_float2(u.x, u.y));
+    f[1] = add2(f[1], make_float2(u.z, u.w));
+    f[2] = add2(f[2], make_float2(v.x, v.y));
+    f[3] = add2(f[3], make_float2(v.z, v.w));
+  }
+  const uint32_t b = r / a.by_nrow;
+  const int64_t n = r - b * a.by_nrow.d;
+  const auto at = [&](const OutView& v) {
+    return reinterpret_cast<uint4*>(v.ptr + b * v.sb + n * v.sn + col_offset(v, col));
+  };
+  if (kOrder == kForward) {
+    if (a.bias != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float* bf = static_cast<const float*>(a.bias) + col + 2 * e;
+        const uint16_t* bh = static_cast<const uint16_t*>(a.bias) + col + 2 * e;
+        f[e] = add2(f[e], a.bias_f32 ? make_float2(bf[0], bf[1])
+                                     : make_float2(__uint_as_float(uint32_t(bh[0]) << 16),
+                                                   __uint_as_float(uint32_t(bh[1]) << 16)));
+      }
+    }
+    if (a.pre.ptr != nullptr) *at(a.pre) = pack(f);
+    act_run(a.act, f);
+  }
+  if (kOrder != kWgrad && a.res.ptr != nullptr) {
+    float2 x[4];
+    unpack(*at(a.res), x);
+    if (kOrder == kForward) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = add2(f[e], x[e]);
+    } else {
+      slope_run(a.act, x, f);
+    }
+  }
+  *at(a.y) = pack(f);
 }
 
 // Column sums of dy [B, heads, N, D] -> fp32 [O]: a block takes 256 columns (32 lanes of 8) of a
@@ -945,45 +970,50 @@ Cols cols_of(const View& v) { return Cols{v.D, (v.D + kBK - 1) / kBK}; }
 
 int sms(const vsa_plan_s* p) { return p->num_sms > 0 ? p->num_sms : 148; }
 
-int pairs_of(const vsa_plan_s* p) { return sms(p) / 2; }
+int pairs_of(const vsa_plan_s* p) { return std::max(1, sms(p) / 2); }
 
-// Columns of a tile (256 or 128) and splits of the K blocks, by the time they should take, in us:
-// a wave of tiles over the pairs of SMs takes 0.35 a K block with 256 columns and 0.25 with 128
-// (measured: 29 and 20 us at K = 5,376; a tile of 128 columns wants half as much again of operand
-// bytes a product), and 2.5 for its start and end; a split costs the join, a launch and two
-// passes over its fp32 partial sums at some 4 TB/s.
+// Columns of a tile (256 or 128), and into how many splits of K the tiles go that are over after
+// the full waves, by the time it should take, in us: a wave of tiles over the pairs of SMs takes
+// 0.35 a K block with 256 columns and 0.25 with 128 (measured: 29 and 20 us at K = 5,376; a
+// tile of 128 columns wants half as much again of operand bytes a product) and one for its
+// turn; splits cost the join, a launch and two passes over their fp32 partial sums at some 4 TB/s.
 struct Tiling {
-  int bn, splits;
+  int bn, splits, k_split;
+  int64_t whole, split_tiles;
+  size_t bytes() const {
+    return splits > 1 ? size_t(splits) * size_t(split_tiles) * kBM * size_t(bn) * sizeof(float) : 0;
+  }
 };
 Tiling tiling(const vsa_plan_s* p, int64_t m_tiles, int64_t M, int cols, int k_blocks, bool may_split) {
-  Tiling best = {256, 1};
+  Tiling best = {256, 1, k_blocks, 0, 0};
   double least = 1e300;
-  for (const int bn : {256, 128})
-    for (int s = 1; s <= (may_split ? std::min(16, k_blocks / 4) : 1) || s == 1; ++s) {
-      const int64_t tiles = m_tiles * ((cols + bn - 1) / bn) * s;
-      const int64_t waves = (tiles + pairs_of(p) - 1) / pairs_of(p);
-      if (s > 1 && waves > 1) break;
-      const double join = s > 1 ? 3.0 + double(s) * double(M) * cols * 8 / 4e6 : 0.0;
-      const double t = double(waves) * (((k_blocks + s - 1) / s) * (bn == 256 ? 0.35 : 0.25) + 2.5) + join;
+  for (const int bn : {256, 128}) {
+    const int64_t tiles = m_tiles * ((cols + bn - 1) / bn), rest = tiles % pairs_of(p);
+    const double block = bn == 256 ? 0.35 : 0.25;
+    const int most = may_split && rest > 0
+                         ? int(std::min<int64_t>({16, k_blocks / 4, pairs_of(p) / rest}))
+                         : 1;
+    for (int want = 1; want <= std::max(1, most); ++want) {
+      const int k_split = (k_blocks + want - 1) / want, s = (k_blocks + k_split - 1) / k_split;
+      const double join = s > 1 ? 3.0 + double(s) * double(rest) * double(std::min<int64_t>(M, kBM)) * bn * 8 / 4e6 : 0.0;
+      const double t = double(tiles / pairs_of(p)) * (k_blocks * block + 1) +
+                       (rest > 0 ? k_split * block + 1 : 0) + join;
       if (t < least) {
         least = t;
-        best = {bn, s};
+        best = {bn, s, k_split, s > 1 ? tiles - rest : tiles, s > 1 ? rest : 0};
       }
     }
+  }
   return best;
 }
-// fp32 partial products of `splits`, in bytes.
-size_t split_bytes(int splits, int64_t M, int cols) {
-  return splits > 1 ? (size_t(splits) * size_t(M) * size_t(cols) * sizeof(float) + 15) / 16 * 16 : 0;
-}
 
-// Tiles of the output and splits of the K blocks, evenly; no split is left without one.
 void set_tiles(const vsa_plan_s* p, GemmArgs* a, bool may_split) {
   const Tiling t = tiling(p, a->m_tiles, a->M, a->cols, a->k_blocks, may_split);
   a->bn = t.bn;
   a->n_tiles = (a->cols + t.bn - 1) / t.bn;
-  a->k_split = (a->k_blocks + t.splits - 1) / t.splits;
-  a->splits = (a->k_blocks + a->k_split - 1) / a->k_split;
+  a->k_split = t.k_split;
+  a->splits = t.splits;
+  a->whole = int(t.whole);
 }
 
 int row_blocks(const View& v, int rows) { return int((v.N + rows - 1) / rows); }
@@ -998,6 +1028,8 @@ int colsum_runs(int64_t M) { return int(std::max<int64_t>(1, (M + colsum_rows(M)
 template <int kOrder>
 vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv, int b_box,
                   GemmArgs a, int64_t b_bytes, cudaStream_t stream) {
+  if (int64_t(a.m_tiles) * a.n_tiles >= (int64_t(1) << 31))
+    return fail(VSA_ERR_UNSUPPORTED, "too many output tiles");
   CUtensorMap ma, mb;
   if (!map_view(&ma, av, a_box) || !map_view(&mb, bv, b_box))
     return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
@@ -1013,15 +1045,12 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
   a.by_rows_b = make_div(a.rows_b);
   a.by_nrow = make_div(a.Nrow);
   a.status = p->d_status;
-  const int64_t tiles = int64_t(a.m_tiles) * a.n_tiles * a.splits;
-  if (tiles >= (int64_t(1) << 31)) return fail(VSA_ERR_UNSUPPORTED, "too many output tiles");
-  const int grid = 2 * int(std::min<int64_t>(tiles, pairs_of(p)));
+  const int64_t rest = int64_t(a.m_tiles) * a.n_tiles - a.whole, items = a.whole + rest * a.splits;
+  const int grid = 2 * int(std::min<int64_t>(items, pairs_of(p)));
   linear_kernel<kOrder><<<grid, kThreads, kSmem, stream>>>(ma, mb, a);
   e = cudaGetLastError();
   if (e == cudaSuccess && a.splits > 1) {
-    const int64_t octets = a.M * (a.cols / 8);
-    const int blocks = int(std::min<int64_t>((octets + 255) / 256, int64_t(sms(p)) * 8));
-    split_join_kernel<kOrder><<<blocks, 256, 0, stream>>>(a, make_div(a.cols / 8));
+    split_join_kernel<kOrder><<<int(rest) * (kBM * a.bn / 2048), 256, 0, stream>>>(a);
     e = cudaGetLastError();
   }
   return e == cudaSuccess ? VSA_OK
@@ -1061,7 +1090,7 @@ size_t linear_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
   // tiles and K blocks of either flattening, rows or heads
   const int64_t m1 = (M + kBM - 1) / kBM, m2 = int64_t(B) * ((N + kBM - 1) / kBM);
   const int kb = (C + kBK - 1) / kBK;
-  return split_bytes(std::max(tiling(p, m1, M, O, kb, true).splits, tiling(p, m2, M, O, kb, true).splits), M, O);
+  return std::max(tiling(p, m1, M, O, kb, true).bytes(), tiling(p, m2, M, O, kb, true).bytes());
 }
 
 vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, void* ws, cudaStream_t stream) {
@@ -1089,6 +1118,7 @@ vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, void* ws
 }
 
 size_t linear_backward_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
+  if (int64_t(B) * N == 0) return 0;
   // one buffer, used in turn by the products' partial sums and the column sums; tiles and K blocks of
   // either flattening, rows or heads
   const int64_t M = int64_t(B) * N;
@@ -1096,9 +1126,8 @@ size_t linear_backward_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O
   const int64_t k1 = (M + kBK - 1) / kBK, k2 = int64_t(B) * ((N + kBK - 1) / kBK);
   const int ko = (O + kBK - 1) / kBK;
   const int64_t mo = (O + kBM - 1) / kBM;
-  const int dgrad = std::max(tiling(p, m1, M, C, ko, true).splits, tiling(p, m2, M, C, ko, true).splits);
-  const int wgrad = std::max(tiling(p, mo, O, C, int(k1), true).splits, tiling(p, mo, O, C, int(k2), true).splits);
-  return std::max({split_bytes(dgrad, M, C), split_bytes(wgrad, O, C),
+  return std::max({tiling(p, m1, M, C, ko, true).bytes(), tiling(p, m2, M, C, ko, true).bytes(),
+                   tiling(p, mo, O, C, int(k1), true).bytes(), tiling(p, mo, O, C, int(k2), true).bytes(),
                    size_t(colsum_runs(M)) * O * sizeof(float)});
 }
 
