@@ -78,8 +78,8 @@ vsa_status vsa_rope_destroy(vsa_rope rope);
  * x, y bf16 [B,H,N,D] in natural order, N the plan's tokens.  fp32 arithmetic,
  * one rounding.  y may be x itself (same pointer and strides); otherwise they
  * must not overlap. */
-vsa_status vsa_rope_apply(vsa_plan plan, vsa_rope rope, vsa_view x, vsa_view y, int inverse, int B,
-                          int H, int D, void* stream);
+vsa_status vsa_rope_apply(vsa_plan plan, vsa_rope rope, const vsa_view* x, const vsa_view* y,
+                          int inverse, int B, int H, int D, void* stream);
 
 /* --------------------------------------------------------------- norm_rope
  * Per head and token, over the D channels:

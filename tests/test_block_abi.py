@@ -80,17 +80,17 @@ def test_rope_refusals(libvsa, bad, status):
 def test_host_only_plan_refuses_launches(libvsa):
     plan = vsa.Plan((40, 70), (4, 8, 8), (4, 4, 4), device=-1)
     rope = vsa.Rope(plan, (24, 20, 20))
-    v = vsa._View(0x1000, 8, 8, 64)
+    v = vsa._VIEW.pack(0x1000, 8, 8, 64)
     L = libvsa
     assert L.vsa_rope_apply(plan.handle, rope.handle, v, v, 0, 1, 1, 64, None) == 1
     assert b"host-only" in L.vsa_last_error()
-    t = (vsa._HeadTensor * 1)()
+    t = bytes(vsa._HEAD_TENSOR.size)
     assert L.vsa_norm_rope(plan.handle, rope.handle, t, 1, 1e-6, 1, 1, 64, None) == 1
     assert L.vsa_norm_rope_permute_pool(plan.handle, rope.handle, t, 1, 1e-6, 1, 1, 64, None) == 1
-    g = (vsa._HeadGrad * 1)()
+    g = bytes(vsa._HEAD_GRAD.size)
     assert L.vsa_norm_rope_backward(plan.handle, rope.handle, g, 1, 1e-6, 0, 1, 1, 64, None, 0, None) == 1
-    assert L.vsa_linear(plan.handle, ctypes.byref(vsa._LinearArgs()), None, 0, None) == 1
-    assert L.vsa_linear_backward(plan.handle, ctypes.byref(vsa._LinearGradArgs()), None, 0, None) == 1
+    assert L.vsa_linear(plan.handle, bytes(vsa._LINEAR.size), None, 0, None) == 1
+    assert L.vsa_linear_backward(plan.handle, bytes(vsa._LINEAR_GRAD.size), None, 0, None) == 1
     assert L.vsa_act_backward(plan.handle, None, None, 0, None, 8, None) == 1
     assert b"host-only" in L.vsa_last_error()
     assert L.vsa_rope_apply(None, rope.handle, v, v, 0, 1, 1, 64, None) == 1
@@ -117,6 +117,33 @@ def test_host_only_plan_refuses_launches(libvsa):
     plan.close()
     assert rope.tables()[0].shape == (366, 32)
     rope.close()
+
+
+def test_records_match_the_header(libvsa):
+    """The packed records have the sizes and offsets a C compiler gives the header's structures."""
+    import subprocess
+    import tempfile
+    code = '''#include <stddef.h>
+#include <stdio.h>
+#include "vsa_block.h"
+int main() {
+  printf("%zu %zu %zu %zu %zu %zu\\n", sizeof(vsa_view), sizeof(vsa_head_tensor), sizeof(vsa_head_grad),
+         sizeof(vsa_linear_args), sizeof(vsa_linear_grad_args), sizeof(vsa_rope_desc));
+  printf("%zu %zu %zu %zu %zu\\n", offsetof(vsa_head_tensor, y), offsetof(vsa_head_grad, dx),
+         offsetof(vsa_linear_args, bias_type), offsetof(vsa_linear_grad_args, x_act),
+         offsetof(vsa_linear_grad_args, dx));
+}'''
+    with tempfile.TemporaryDirectory() as d:
+        src, exe = os.path.join(d, "s.c"), os.path.join(d, "s")
+        open(src, "w").write(code)
+        subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), src, "-o", exe], check=True)
+        sizes, offsets = (list(map(int, ln.split())) for ln in
+                          subprocess.run([exe], capture_output=True, text=True).stdout.splitlines())
+    assert sizes == [vsa._VIEW.size, vsa._HEAD_TENSOR.size, vsa._HEAD_GRAD.size, vsa._LINEAR.size,
+                     vsa._LINEAR_GRAD.size, ctypes.sizeof(vsa._RopeDesc)]
+    S = lambda f: vsa.struct.calcsize("@" + f + "0P")
+    assert offsets == [S("PqqqPiii"), S("PqqqPqqqPiii"), vsa.struct.calcsize("@iiiiiqPqqqPP"),
+                       vsa.struct.calcsize("@iiiiiqPqqqPqqqPPqqq"), S("iiiiiqPqqqPqqqPPqqqi")]
 
 
 def _diff(f, x, d, h=1e-5):

@@ -4,8 +4,6 @@ oracle, and their refusals.
 Tolerances.  A bf16 output is one rounding, at most 2^-8 of its value (half of
 finfo(bfloat16).eps), of an fp32 result; what fp32 adds is bounded beside each check
 by the magnitudes that enter it (2^-24 an operation; 2^-22 the reciprocal root)."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -292,11 +290,10 @@ def test_linear(c, act):
     close(y, BO.heads(want, yh), BO.heads(s, yh), "y")
     # without a workspace the K blocks are not split
     yw = torch.empty_like(y)
-    a = vsa._LinearArgs(B=B, x_heads=xh, C=C, y_heads=yh, O=Ow, N=N, act=vsa.ACTS[act])
-    a.x, a.y, a.w = vsa._view(plan, x, "x", x.shape), vsa._view(plan, yw, "y", y.shape), w.data_ptr()
-    a.bias, a.bias_type = vsa._vector(plan, bias, "bias", Ow)
-    a.residual = vsa._view(plan, res, "residual", res.shape)
-    assert vsa.lib().vsa_linear(plan.handle, ctypes.byref(a), None, 0, vsa._stream(None)) == 0
+    xv, yv, rv = (vsa._view(plan, t, "t", t.shape) for t in (x, yw, res))
+    args = vsa._LINEAR.pack(B, xh, C, yh, Ow, N, *xv, w.data_ptr(), *vsa._vector(plan, bias, "bias", Ow),
+                            vsa.ACTS[act], *rv, *vsa._NO_VIEW, *yv)
+    assert vsa.lib().vsa_linear(plan.handle, args, None, 0, vsa._raw_stream(plan, None)) == 0
     close(yw, BO.heads(want, yh), BO.heads(s, yh), "no workspace")
     # without bias and residual; the residual read from y itself
     y2 = vsa.vsa_linear(plan, x, w, act=act, y_heads=yh)
@@ -416,8 +413,8 @@ def test_linear_refusals():
     with pytest.raises(ValueError):
         vsa.vsa_linear_backward(plan, torch.zeros(1, 9, 128, **bf), x, w, x_act="silu")
     # plain C: unknown codes
-    a = vsa._LinearArgs(B=1, C=64, O=128, N=9, act=7)
-    assert vsa.lib().vsa_linear(plan.handle, ctypes.byref(a), None, 0, None) == 1
-    a = vsa._LinearArgs(B=1, C=64, O=128, N=9, bias_type=2)
-    assert vsa.lib().vsa_linear(plan.handle, ctypes.byref(a), None, 0, None) == 1
+    none = vsa._NO_VIEW
+    for bias_type, act in ((0, 7), (2, 0), (0, -1)):
+        args = vsa._LINEAR.pack(1, 0, 64, 0, 128, 9, *none, 0, 0, bias_type, act, *none, *none, *none)
+        assert vsa.lib().vsa_linear(plan.handle, args, None, 0, None) == 1
     vsa.vsa_sync_status(plan)

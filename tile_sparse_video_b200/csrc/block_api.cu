@@ -306,10 +306,12 @@ vsa_status vsa_rope_destroy(vsa_rope r) {
   return VSA_OK;
 }
 
-vsa_status vsa_rope_apply(vsa_plan p, vsa_rope rope, vsa_view x, vsa_view y, int inverse, int B,
-                          int H, int D, void* stream) {
+vsa_status vsa_rope_apply(vsa_plan p, vsa_rope rope, const vsa_view* xv, const vsa_view* yv, int inverse,
+                          int B, int H, int D, void* stream) {
   VSA_NVTX_RANGE();
   VSA_TRY(check_heads(p, B, H, D));
+  if (xv == nullptr || yv == nullptr) return fail(VSA_ERR_INVALID_ARG, "x or y is NULL");
+  const vsa_view x = *xv, y = *yv;
   VSA_TRY(check_rope(p, rope, D));
   if (inverse != 0 && inverse != 1) return fail(VSA_ERR_INVALID_ARG, "inverse must be 0 or 1");
   if (int64_t(B) * H == 0 || p->n_tokens == 0) return VSA_OK;

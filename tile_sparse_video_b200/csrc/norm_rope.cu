@@ -480,8 +480,11 @@ bool set_items(Args* a, const vsa_plan_s* p, int64_t row_blocks, int B, int H, i
 template <class Kernel, class Args>
 cudaError_t launch(Kernel k, int64_t items, int n, int threads, uint32_t smem, const Args& a,
                    cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
+  // 48 KB need no leave, less the 4 KB a kernel has besides
+  if (smem > 44 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+  }
   k<<<dim3(unsigned(items), unsigned(n)), threads, smem, stream>>>(a);
   return cudaGetLastError();
 }

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple, Optional, Sequence
 
 import numpy as np
@@ -58,9 +59,19 @@ class _Geometry(ctypes.Structure):
                 ("tile_t", ctypes.c_int32), ("tile_h", ctypes.c_int32), ("tile_w", ctypes.c_int32)]
 
 
-class _View(ctypes.Structure):
-    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
-                ("stride_n", ctypes.c_int64)]
+class _RopeDesc(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32 * 3), ("halves", ctypes.c_int32), ("theta", ctypes.c_double * 3),
+                ("offset", ctypes.c_double * 3), ("step", ctypes.c_double * 3),
+                ("inv_freq", ctypes.c_void_p), ("prefix_pos", ctypes.c_void_p)]
+
+
+# Records of include/vsa_block.h, packed by the platform's C rules (a ctypes structure of
+# views costs more host time a call than the launch).  A view is "Pqqq".
+_VIEW = struct.Struct("@Pqqq")
+_HEAD_TENSOR = struct.Struct("@PqqqPiiiPqqqP")
+_HEAD_GRAD = struct.Struct("@PqqqPqqqPiiiPqqqP")
+_LINEAR = struct.Struct("@iiiiiqPqqqPPiiPqqqPqqqPqqq")
+_LINEAR_GRAD = struct.Struct("@iiiiiqPqqqPqqqPPqqqiPqqqPP")
 
 
 class _RopeDesc(ctypes.Structure):
@@ -69,30 +80,13 @@ class _RopeDesc(ctypes.Structure):
                 ("inv_freq", ctypes.c_void_p), ("prefix_pos", ctypes.c_void_p)]
 
 
-class _HeadTensor(ctypes.Structure):
-    _fields_ = [("x", _View), ("gain", ctypes.c_void_p), ("gain_type", ctypes.c_int32),
-                ("norm", ctypes.c_int32), ("rotate", ctypes.c_int32), ("y", _View),
-                ("pooled", ctypes.c_void_p)]
-
-
-class _HeadGrad(ctypes.Structure):
-    _fields_ = [("dy", _View), ("x", _View), ("gain", ctypes.c_void_p), ("gain_type", ctypes.c_int32),
-                ("norm", ctypes.c_int32), ("rotate", ctypes.c_int32), ("dx", _View),
-                ("d_gain", ctypes.c_void_p)]
-
-
-class _LinearArgs(ctypes.Structure):
-    _fields_ = [("B", ctypes.c_int32), ("x_heads", ctypes.c_int32), ("C", ctypes.c_int32),
-                ("y_heads", ctypes.c_int32), ("O", ctypes.c_int32), ("N", ctypes.c_int64), ("x", _View),
-                ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("bias_type", ctypes.c_int32),
-                ("act", ctypes.c_int32), ("residual", _View), ("pre", _View), ("y", _View)]
-
-
-class _LinearGradArgs(ctypes.Structure):
-    _fields_ = [("B", ctypes.c_int32), ("x_heads", ctypes.c_int32), ("C", ctypes.c_int32),
-                ("y_heads", ctypes.c_int32), ("O", ctypes.c_int32), ("N", ctypes.c_int64), ("dy", _View),
-                ("x", _View), ("w", ctypes.c_void_p), ("x_pre", _View), ("x_act", ctypes.c_int32),
-                ("dx", _View), ("dw", ctypes.c_void_p), ("db", ctypes.c_void_p)]
+# Records of include/vsa_block.h, packed by the platform's C rules (a ctypes structure of
+# views costs more host time a call than the launch).  A view is "Pqqq".
+_VIEW = struct.Struct("@Pqqq")
+_HEAD_TENSOR = struct.Struct("@PqqqPiiiPqqqP")
+_HEAD_GRAD = struct.Struct("@PqqqPqqqPiiiPqqqP")
+_LINEAR = struct.Struct("@iiiiiqPqqqPPiiPqqqPqqqPqqq")
+_LINEAR_GRAD = struct.Struct("@iiiiiqPqqqPqqqPPqqqiPqqqPP")
 
 
 def lib():
@@ -143,15 +137,15 @@ def lib():
             "vsa_rope_create": [P, ctypes.POINTER(_RopeDesc), ctypes.POINTER(P)],
             "vsa_rope_tables": [P, ctypes.POINTER(I32), V],
             "vsa_rope_destroy": [P],
-            "vsa_rope_apply": [P, P, _View, _View, I, I, I, I, V],
-            "vsa_norm_rope": [P, P, ctypes.POINTER(_HeadTensor), I, F, I, I, I, V],
-            "vsa_norm_rope_permute_pool": [P, P, ctypes.POINTER(_HeadTensor), I, F, I, I, I, V],
+            "vsa_rope_apply": [P, P, V, V, I, I, I, I, V],
+            "vsa_norm_rope": [P, P, V, I, F, I, I, I, V],
+            "vsa_norm_rope_permute_pool": [P, P, V, I, F, I, I, I, V],
             "vsa_norm_rope_backward_workspace_size": [P, I, I, ctypes.POINTER(Z)],
-            "vsa_norm_rope_backward": [P, P, ctypes.POINTER(_HeadGrad), I, F, I, I, I, I, V, Z, V],
+            "vsa_norm_rope_backward": [P, P, V, I, F, I, I, I, I, V, Z, V],
             "vsa_linear_workspace_size": [P, I, I64, I, I, ctypes.POINTER(Z)],
-            "vsa_linear": [P, ctypes.POINTER(_LinearArgs), V, Z, V],
+            "vsa_linear": [P, V, V, Z, V],
             "vsa_linear_backward_workspace_size": [P, I, I64, I, I, ctypes.POINTER(Z)],
-            "vsa_linear_backward": [P, ctypes.POINTER(_LinearGradArgs), V, Z, V],
+            "vsa_linear_backward": [P, V, V, Z, V],
             "vsa_act_backward": [P, V, V, I, V, I64, V],
         }
         for name, args in sig.items():
@@ -210,6 +204,7 @@ class Plan:
         _check(L.vsa_plan_create(ctypes.byref(geo), int(device), ctypes.byref(h)))
         self._h = h
         self.device = int(device)
+        self.sizes = {}                  # workspace sizes by query (see _workspace_bytes)
         n_tok, n_pad = ctypes.c_int64(), ctypes.c_int64()
         T, n_p, R = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
         _check(L.vsa_plan_info(h, ctypes.byref(n_tok), ctypes.byref(n_pad), ctypes.byref(T),
@@ -627,44 +622,56 @@ def vsa_sparse_attn_backward(plan: Plan, q_t, k_t, v_t, d_out_t, topk_idx, k: in
 # ------------------------------------------------- the operators around the layer
 # (include/vsa_block.h)
 
-def _on_plan(plan: Plan, t: torch.Tensor, name: str, dtype=torch.bfloat16):
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_NO_VIEW = (0, 0, 0, 0)
+
+
+def _raw_stream(plan: Plan, stream) -> int:
+    """The stream's handle; without one, the current stream of the plan's device."""
+    return torch._C._cuda_getCurrentRawStream(plan.device) if stream is None else stream.cuda_stream
+
+
+def _on_plan(plan: Plan, t: torch.Tensor, name: str, dtype=_BF16):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.get_device() != plan.device:
+    if t.get_device() != plan.device:
         raise ValueError(f"{name} must be on the plan's device, cuda:{plan.device}")
 
 
-def _view(plan: Plan, t: Optional[torch.Tensor], name: str, shape) -> _View:
-    """A strided bf16 tensor [B,H,N,D] or [B,N,C] as a vsa_view."""
+def _view(plan: Plan, t: Optional[torch.Tensor], name: str, shape) -> tuple:
+    """A strided bf16 tensor [B,H,N,D] or [B,N,C] as the fields of a vsa_view."""
     if t is None:
-        return _View(None, 0, 0, 0)
-    _on_plan(plan, t, name)
-    if tuple(t.shape) != tuple(shape):
+        return _NO_VIEW
+    if type(t) is not torch.Tensor or t.dtype is not _BF16 or t.get_device() != plan.device:
+        _on_plan(plan, t, name)
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     s = t.stride()
-    if s[-1] != 1 and t.numel() > 0:
+    if s[-1] != 1 and t.numel() > 0 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return _View(t.data_ptr(), s[0], s[1] if len(s) == 4 else 0, s[-2])
+    return (t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else (t.data_ptr(), s[0], 0, s[1])
 
 
 def _vector(plan: Plan, t: Optional[torch.Tensor], name: str, n: int):
     """A contiguous parameter vector [n], bf16 or fp32: (pointer, type)."""
     if t is None:
-        return None, 0
-    _on_plan(plan, t, name, torch.bfloat16 if t.dtype == torch.bfloat16 else torch.float32)
-    if tuple(t.shape) != (n,) or not t.is_contiguous():
+        return 0, 0
+    f32 = t.dtype is not _BF16
+    _on_plan(plan, t, name, _F32 if f32 else _BF16)
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n}")
-    return t.data_ptr(), 1 if t.dtype == torch.float32 else 0
+    return t.data_ptr(), int(f32)
 
 
-def _dense(plan: Plan, t: Optional[torch.Tensor], name: str, dtype, shape):
+def _dense(plan: Plan, t: Optional[torch.Tensor], name: str, dtype, shape) -> int:
     """A contiguous tensor's pointer."""
     if t is None:
-        return None
-    _on_plan(plan, t, name, dtype)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        return 0
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != plan.device:
+        _on_plan(plan, t, name, dtype)
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
     return t.data_ptr()
 
@@ -673,13 +680,24 @@ class _Out:
     """Allocates a call's outputs on the stream that will write them."""
 
     def __init__(self, plan: Plan, stream):
-        self.dev, self.stream = torch.device("cuda", plan.device), stream
+        self.dev, self.stream = plan.device, stream
 
-    def __call__(self, shape, dtype=torch.bfloat16):
+    def __call__(self, shape, dtype=_BF16):
         if self.stream is None:
             return torch.empty(shape, dtype=dtype, device=self.dev)
         with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=self.dev)
+
+
+def _workspace_bytes(plan: Plan, query: str, *sizes: int) -> int:
+    """A workspace's size from its query; a plan keeps the sizes it was asked for."""
+    key = (query, *sizes)
+    n = plan.sizes.get(key)
+    if n is None:
+        b = ctypes.c_size_t()
+        _check(getattr(lib(), query)(plan.handle, *sizes, ctypes.byref(b)))
+        n = plan.sizes[key] = b.value
+    return n
 
 
 class Rope:
@@ -746,11 +764,11 @@ def vsa_rope_apply(plan: Plan, rope: Rope, x: torch.Tensor, y: Optional[torch.Te
     the gradient).  ``y`` may be x."""
     B, H, _, D = x.shape
     shape = (B, H, plan.n_tokens, D)
-    xv = _view(plan, x, "x", shape)
+    xv = _VIEW.pack(*_view(plan, x, "x", shape))
     if y is None:
         y = _Out(plan, stream)(shape)
-    _check(lib().vsa_rope_apply(plan.handle, rope.handle, xv, _view(plan, y, "y", shape), int(inverse),
-                                B, H, D, _stream(stream)))
+    _check(lib().vsa_rope_apply(plan.handle, rope.handle, xv, _VIEW.pack(*_view(plan, y, "y", shape)),
+                                bool(inverse), B, H, D, _raw_stream(plan, stream)))
     return y
 
 
@@ -783,24 +801,25 @@ def _norm_rope(plan, items, rope, eps, tiled, stream):
         raise ValueError(f"1 to {MAX_HEAD_TENSORS} tensors a call")
     B, H, _, D = items[0].x.shape
     natural, out = (B, H, plan.n_tokens, D), _Out(plan, stream)
-    arr, res = (_HeadTensor * len(items))(), []
-    for a, it in zip(arr, items):
-        a.x = _view(plan, it.x, "x", natural)
-        a.gain, a.gain_type = _vector(plan, it.gain, "gain", D)
-        a.norm, a.rotate = int(it.norm), int(it.rotate)
+    tiles, means = (B, H, plan.n_padded, D), (B, H, plan.n_tiles, D)
+    records, res = [], []
+    for x, gain, norm, rotate, y, pooled in items:
+        xv, pv = _view(plan, x, "x", natural), 0
+        gv, gt = _vector(plan, gain, "gain", D)
         if tiled:
-            y = out((B, H, plan.n_padded, D)) if it.y is None else it.y
-            pooled = out((B, H, plan.n_tiles, D), torch.float32) if it.pooled is None else it.pooled
-            a.y.ptr = _dense(plan, y, "y", torch.bfloat16, (B, H, plan.n_padded, D))
-            a.pooled = _dense(plan, pooled, "pooled", torch.float32, (B, H, plan.n_tiles, D))
+            y = out(tiles) if y is None else y
+            pooled = out(means, _F32) if pooled is None else pooled
+            yv = (_dense(plan, y, "y", _BF16, tiles), 0, 0, 0)
+            pv = _dense(plan, pooled, "pooled", _F32, means)
             res.append((y, pooled))
         else:
-            y = out(natural) if it.y is None else it.y
-            a.y = _view(plan, y, "y", natural)
+            y = out(natural) if y is None else y
+            yv = _view(plan, y, "y", natural)
             res.append(y)
+        records.append(_HEAD_TENSOR.pack(*xv, gv, gt, bool(norm), bool(rotate), *yv, pv))
     fn = lib().vsa_norm_rope_permute_pool if tiled else lib().vsa_norm_rope
-    _check(fn(plan.handle, None if rope is None else rope.handle, arr, len(items), eps, B, H, D,
-              _stream(stream)))
+    _check(fn(plan.handle, None if rope is None else rope.handle, b"".join(records), len(items), eps, B,
+              H, D, _raw_stream(plan, stream)))
     return res
 
 
@@ -821,9 +840,8 @@ def vsa_norm_rope_permute_pool(plan: Plan, items: Sequence[HeadTensor], rope: Op
 def norm_rope_backward_workspace(plan: Plan, n: int, D: int) -> torch.Tensor:
     """Workspace of vsa_norm_rope_backward for n tensors (its size comes from
     vsa_norm_rope_backward_workspace_size)."""
-    b = ctypes.c_size_t()
-    _check(lib().vsa_norm_rope_backward_workspace_size(plan.handle, n, D, ctypes.byref(b)))
-    return torch.empty(max(b.value, 16), dtype=torch.uint8, device=torch.device("cuda", plan.device))
+    return _Out(plan, None)((max(_workspace_bytes(plan, "vsa_norm_rope_backward_workspace_size", n, D), 16),),
+                            _U8)
 
 
 def vsa_norm_rope_backward(plan: Plan, items: Sequence[HeadGrad], rope: Optional[Rope] = None,
@@ -835,31 +853,28 @@ def vsa_norm_rope_backward(plan: Plan, items: Sequence[HeadGrad], rope: Optional
         raise ValueError(f"1 to {MAX_HEAD_TENSORS} tensors a call")
     B, H, _, D = items[0].dy.shape
     natural, out = (B, H, plan.n_tokens, D), _Out(plan, stream)
-    arr, res = (_HeadGrad * len(items))(), []
-    for a, it in zip(arr, items):
-        if tiled:
-            a.dy.ptr = _dense(plan, it.dy, "dy", torch.bfloat16, (B, H, plan.n_padded, D))
-        else:
-            a.dy = _view(plan, it.dy, "dy", natural)
-        if it.norm and it.x is None:
+    tiles = (B, H, plan.n_padded, D)
+    records, res = [], []
+    for dy, x, gain, norm, rotate, dx, dg in items:
+        dyv = (_dense(plan, dy, "dy", _BF16, tiles), 0, 0, 0) if tiled else _view(plan, dy, "dy", natural)
+        if norm and x is None:
             raise ValueError("the norm's backward needs x")
-        a.x = _view(plan, it.x if it.norm else None, "x", natural)
-        a.gain, a.gain_type = _vector(plan, it.gain, "gain", D)
-        a.norm, a.rotate = int(it.norm), int(it.rotate)
-        dx = out(natural) if it.dx is None else it.dx
-        a.dx = _view(plan, dx, "dx", natural)
-        dg = it.d_gain
-        if dg is None and it.gain is not None:
-            dg = out((D,), torch.float32)
-        a.d_gain = _dense(plan, dg, "d_gain", torch.float32, (D,))
+        xv = _view(plan, x, "x", natural) if norm else _NO_VIEW
+        gv, gt = _vector(plan, gain, "gain", D)
+        dx = out(natural) if dx is None else dx
+        if dg is None and gain is not None:
+            dg = out((D,), _F32)
+        records.append(_HEAD_GRAD.pack(*dyv, *xv, gv, gt, bool(norm), bool(rotate),
+                                       *_view(plan, dx, "dx", natural),
+                                       _dense(plan, dg, "d_gain", _F32, (D,))))
         res.append((dx, dg))
     if ws is None:
-        n = ctypes.c_size_t()
-        _check(lib().vsa_norm_rope_backward_workspace_size(plan.handle, len(items), D, ctypes.byref(n)))
-        ws = out((max(n.value, 16),), torch.uint8)
-    _check(lib().vsa_norm_rope_backward(plan.handle, None if rope is None else rope.handle, arr,
-                                        len(items), eps, int(tiled), B, H, D, _ptr(ws),
-                                        ws.numel() * ws.element_size(), _stream(stream)))
+        ws = out((max(_workspace_bytes(plan, "vsa_norm_rope_backward_workspace_size", len(items), D), 16),),
+                 _U8)
+    _check(lib().vsa_norm_rope_backward(plan.handle, None if rope is None else rope.handle,
+                                        b"".join(records), len(items), eps, bool(tiled), B, H, D,
+                                        ws.data_ptr(), ws.numel() * ws.element_size(),
+                                        _raw_stream(plan, stream)))
     return res
 
 
@@ -880,12 +895,6 @@ def _sides(t: torch.Tensor, name: str):
     return B, N, 0, C
 
 
-def _linear_bytes(plan: Plan, B: int, N: int, C: int, O: int) -> int:
-    b = ctypes.c_size_t()
-    _check(lib().vsa_linear_workspace_size(plan.handle, B, N, C, O, ctypes.byref(b)))
-    return b.value
-
-
 def vsa_linear(plan: Plan, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
                act: str = "identity", residual: Optional[torch.Tensor] = None, y_heads: int = 0,
                y: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
@@ -901,35 +910,27 @@ def vsa_linear(plan: Plan, x: torch.Tensor, w: torch.Tensor, bias: Optional[torc
     if like is not None:
         y_heads = _sides(like, "y")[2]
     shape = (B, y_heads, N, O // y_heads) if y_heads else (B, N, O)
-    a = _LinearArgs(B=B, x_heads=xh, C=C, y_heads=y_heads, O=O, N=N)
-    a.x = _view(plan, x, "x", x.shape)
-    a.w = _dense(plan, w, "w", torch.bfloat16, (O, C))
-    a.bias, a.bias_type = _vector(plan, bias, "bias", O)
-    a.act = _act(act)
-    a.residual = _view(plan, residual, "residual", shape)
-    a.pre = _view(plan, pre, "pre", shape)
+    xv, rv, pv = (_view(plan, t, name, sh) for t, name, sh in
+                  ((x, "x", x.shape), (residual, "residual", shape), (pre, "pre", shape)))
+    bv, bt = _vector(plan, bias, "bias", O)
     if y is None:
         y = _Out(plan, stream)(shape)
-    a.y = _view(plan, y, "y", shape)
+    args = _LINEAR.pack(B, xh, C, y_heads, O, N, *xv, _dense(plan, w, "w", _BF16, (O, C)), bv, bt,
+                        _act(act), *rv, *pv, *_view(plan, y, "y", shape))
     if ws is None:
-        n = _linear_bytes(plan, B, N, C, O)
-        ws = _Out(plan, stream)((n,), torch.uint8) if n else None
-    _check(lib().vsa_linear(plan.handle, ctypes.byref(a), _ptr(ws),
-                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        n = _workspace_bytes(plan, "vsa_linear_workspace_size", B, N, C, O)
+        ws = _Out(plan, stream)((n,), _U8) if n else None
+    _check(lib().vsa_linear(plan.handle, args, None if ws is None else ws.data_ptr(),
+                            0 if ws is None else ws.numel() * ws.element_size(),
+                            _raw_stream(plan, stream)))
     return y
-
-
-def _linear_backward_bytes(plan: Plan, B: int, N: int, C: int, O: int) -> int:
-    b = ctypes.c_size_t()
-    _check(lib().vsa_linear_backward_workspace_size(plan.handle, B, N, C, O, ctypes.byref(b)))
-    return max(b.value, 16)
 
 
 def linear_backward_workspace(plan: Plan, B: int, N: int, C: int, O: int) -> torch.Tensor:
     """Workspace of vsa_linear_backward (its size comes from
     vsa_linear_backward_workspace_size)."""
-    return torch.empty(_linear_backward_bytes(plan, B, N, C, O), dtype=torch.uint8,
-                       device=torch.device("cuda", plan.device))
+    n = _workspace_bytes(plan, "vsa_linear_backward_workspace_size", B, N, C, O)
+    return _Out(plan, None)((max(n, 16),), _U8)
 
 
 def vsa_linear_backward(plan: Plan, dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
@@ -943,36 +944,32 @@ def vsa_linear_backward(plan: Plan, dy: torch.Tensor, x: torch.Tensor, w: torch.
     B, N, xh, C = _sides(x, "x")
     _, _, yh, O = _sides(dy, "dy")
     out = _Out(plan, stream)
-    a = _LinearGradArgs(B=B, x_heads=xh, C=C, y_heads=yh, O=O, N=N)
-    a.dy = _view(plan, dy, "dy", (B, yh, N, O // yh) if yh else (B, N, O))
-    a.x = _view(plan, x, "x", x.shape)
-    a.w = _dense(plan, w, "w", torch.bfloat16, (O, C))
-    a.x_pre = _view(plan, x_pre, "x_pre", x.shape)
-    a.x_act = _act(x_act)
-    if x_pre is None and a.x_act:
+    dyv = _view(plan, dy, "dy", (B, yh, N, O // yh) if yh else (B, N, O))
+    xv, xpv = _view(plan, x, "x", x.shape), _view(plan, x_pre, "x_pre", x.shape)
+    act = _act(x_act)
+    if x_pre is None and act:
         raise ValueError("x_act needs x_pre")
     dx = (out(x.shape) if dx is None else dx) if need[0] else None
     dw = (out((O, C)) if dw is None else dw) if need[1] else None
-    db = (out((O,), torch.float32) if db is None else db) if need[2] else None
-    a.dx = _view(plan, dx, "dx", x.shape)
-    a.dw = _dense(plan, dw, "dw", torch.bfloat16, (O, C))
-    a.db = _dense(plan, db, "db", torch.float32, (O,))
+    db = (out((O,), _F32) if db is None else db) if need[2] else None
+    args = _LINEAR_GRAD.pack(B, xh, C, yh, O, N, *dyv, *xv, _dense(plan, w, "w", _BF16, (O, C)), *xpv, act,
+                             *_view(plan, dx, "dx", x.shape), _dense(plan, dw, "dw", _BF16, (O, C)),
+                             _dense(plan, db, "db", _F32, (O,)))
     if ws is None:
-        ws = out((_linear_backward_bytes(plan, B, N, C, O),), torch.uint8)
-    _check(lib().vsa_linear_backward(plan.handle, ctypes.byref(a), _ptr(ws),
-                                     ws.numel() * ws.element_size(), _stream(stream)))
+        ws = out((max(_workspace_bytes(plan, "vsa_linear_backward_workspace_size", B, N, C, O), 16),), _U8)
+    _check(lib().vsa_linear_backward(plan.handle, args, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                     _raw_stream(plan, stream)))
     return dx, dw, db
 
 
 def vsa_act_backward(plan: Plan, dy: torch.Tensor, pre: torch.Tensor, act: str,
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dy * act'(pre), element by element (contiguous bf16 tensors of one shape)."""
-    d = _dense(plan, dy, "dy", torch.bfloat16, dy.shape)
-    p = _dense(plan, pre, "pre", torch.bfloat16, dy.shape)
+    d, p = _dense(plan, dy, "dy", _BF16, dy.shape), _dense(plan, pre, "pre", _BF16, dy.shape)
     if out is None:
         out = _Out(plan, stream)(dy.shape)
-    o = _dense(plan, out, "out", torch.bfloat16, dy.shape)
-    _check(lib().vsa_act_backward(plan.handle, d, p, _act(act), o, dy.numel(), _stream(stream)))
+    _check(lib().vsa_act_backward(plan.handle, d, p, _act(act), _dense(plan, out, "out", _BF16, dy.shape),
+                                  dy.numel(), _raw_stream(plan, stream)))
     return out
 
 
