@@ -96,7 +96,7 @@ typedef struct vsa_head_tensor {
   int32_t norm, rotate;
   vsa_view y;          /* vsa_norm_rope: bf16 [B,H,N,D]; permute_pool: ptr only, bf16
                           [B,H,N_pad,D] contiguous                                     */
-  float* pooled;       /* permute_pool only: fp32 [B,H,T,D]                            */
+  float* pooled;       /* permute_pool only: fp32 [B,H,T,D], or NULL: no means         */
 } vsa_head_tensor;
 
 /* One launch for n tensors (1 .. VSA_MAX_HEAD_TENSORS), natural order in and out.
@@ -177,6 +177,7 @@ typedef struct vsa_linear_grad_args {
   vsa_view dx;         /* laid out as x, or ptr = NULL                             */
   void* dw;            /* bf16 [O,C], or NULL                                      */
   float* db;           /* fp32 [O], or NULL                                        */
+  vsa_view dx_add;     /* laid out as x, or ptr = NULL: added to dx                */
 } vsa_linear_grad_args;
 
 /* Bytes of workspace of vsa_linear_backward.  Nothing in it has to be set. */
@@ -184,7 +185,9 @@ vsa_status vsa_linear_backward_workspace_size(vsa_plan plan, int B, int64_t N, i
                                               size_t* bytes);
 
 /* dx = dy w, times x_act'(x_pre) when x_pre is given (the gradient then goes
- * through the activation that made x, in the product's epilogue);
+ * through the activation that made x, in the product's epilogue), or plus dx_add
+ * (what reaches x by another way, a residual connection for instance; dx_add may be dx
+ * itself, and does not go with x_pre);
  * dw = dy^T x, db = column sums of dy.  fp32 accumulation in a fixed order.  The
  * gradient of vsa_linear's residual is dy of its output itself.  With no rows dw
  * and db are 0. */

@@ -131,7 +131,7 @@ int main() {
          sizeof(vsa_linear_args), sizeof(vsa_linear_grad_args), sizeof(vsa_rope_desc));
   printf("%zu %zu %zu %zu %zu\\n", offsetof(vsa_head_tensor, y), offsetof(vsa_head_grad, dx),
          offsetof(vsa_linear_args, bias_type), offsetof(vsa_linear_grad_args, x_act),
-         offsetof(vsa_linear_grad_args, dx));
+         offsetof(vsa_linear_grad_args, dx_add));
 }'''
     with tempfile.TemporaryDirectory() as d:
         src, exe = os.path.join(d, "s.c"), os.path.join(d, "s")
@@ -143,7 +143,7 @@ int main() {
                      vsa._LINEAR_GRAD.size, ctypes.sizeof(vsa._RopeDesc)]
     S = lambda f: vsa.struct.calcsize("@" + f + "0P")
     assert offsets == [S("PqqqPiii"), S("PqqqPqqqPiii"), vsa.struct.calcsize("@iiiiiqPqqqPP"),
-                       vsa.struct.calcsize("@iiiiiqPqqqPqqqPPqqq"), S("iiiiiqPqqqPqqqPPqqqi")]
+                       vsa.struct.calcsize("@iiiiiqPqqqPqqqPPqqq"), S("iiiiiqPqqqPqqqPPqqqiPqqqPP")]
 
 
 def _diff(f, x, d, h=1e-5):

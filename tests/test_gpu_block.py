@@ -418,3 +418,33 @@ def test_linear_refusals():
         args = vsa._LINEAR.pack(1, 0, 64, 0, 128, 9, *none, 0, 0, bias_type, act, *none, *none, *none)
         assert vsa.lib().vsa_linear(plan.handle, args, None, 0, None) == 1
     vsa.vsa_sync_status(plan)
+
+
+@linears
+def test_linear_backward_dx_add(c):
+    """dx_add is added before the one rounding; it may be dx itself; not with x_pre."""
+    B, N, xh, C, yh, Ow = c
+    plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4))
+    x, w, dy = rows_or_heads(1, B, N, xh, C), randn(2, Ow, C, scale=0.1), rows_or_heads(5, B, N, yh, Ow)
+    add = rows_or_heads(6, B, N, xh, C)
+    dx, _, _ = vsa.vsa_linear_backward(plan, dy, x, w, dx_add=add, need=(True, False, False))
+    want = BO.linear_backward(dy, x, w)[0] + BO.rows(add)
+    slack = dot_slack(BO.rows(dy), f64(w).T) + 2.0 ** -23 * np.abs(want)
+    close(dx, BO.heads(want, xh), BO.heads(slack, xh), "dx")
+    same = add.clone()
+    vsa.vsa_linear_backward(plan, dy, x, w, dx=same, dx_add=same, need=(True, False, False))
+    assert torch.equal(same, dx)
+    with pytest.raises(vsa.VsaError) as e:
+        vsa.vsa_linear_backward(plan, dy, x, w, x_pre=x, x_act="silu", dx_add=add)
+    assert e.value.status == 1
+    vsa.vsa_sync_status(plan)
+
+
+def test_permute_pool_without_means():
+    plan = vsa.Plan((9, 3), (2, 5, 4), (4, 4, 4))
+    q, g = randn(1, 2, 3, plan.n_tokens, 64), randn(2, 2, 3, plan.n_tokens, 64)
+    (q_t, qbar), (g_t, none) = vsa.vsa_norm_rope_permute_pool(
+        plan, [vsa.HeadTensor(q, rotate=False), vsa.HeadTensor(g, norm=False, rotate=False, pooled=False)])
+    assert none is None and torch.equal(g_t, vsa.vsa_permute(plan, g))
+    assert torch.equal(qbar, vsa.vsa_norm_rope_permute_pool(plan, [vsa.HeadTensor(q, rotate=False)])[0][1])
+    vsa.vsa_sync_status(plan)

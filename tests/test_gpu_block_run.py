@@ -1,0 +1,235 @@
+"""The operators around the layer in use: the attention half of a transformer block, forward
+and backward, each stage against its fp64 oracle on the GPU's own bf16 inputs of that stage,
+and the whole block's gradient against differences of the fp64 forward; then the ways a
+program runs them (other streams, graphs, two at once)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from oracle import block_oracle as BO
+from tests.parity import assert_close, f64
+from tests.test_gpu_block import close, dot_slack, randn
+from tests.test_gpu_backward import assert_rel
+from tile_sparse_video_b200 import vsa
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda(libvsa):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+    yield
+    torch.cuda.synchronize()
+
+
+class Case:
+    def __init__(self, prefix, grid, tile, B, H, D, C, dims, halves, keep, seed):
+        self.B, self.H, self.D, self.C, self.keep = B, H, D, C, keep
+        self.plan = vsa.Plan(prefix, grid, tile)
+        self.p = O.plan(prefix, grid, tile)
+        self.N = self.plan.n_tokens
+        self.rope = vsa.Rope(self.plan, dims, halves=halves)
+        self.ang, self.halves = BO.angles(BO.positions(prefix, grid), dims), halves
+        self.x = randn(seed, B, self.N, C)
+        self.w_in = randn(seed + 1, 4 * H * D, C, scale=C ** -0.5)
+        self.w_out = randn(seed + 2, C, H * D, scale=(H * D) ** -0.5)
+        self.b_in, self.b_out = randn(seed + 3, 4 * H * D, scale=0.1), randn(seed + 4, C, scale=0.1).float()
+        self.gq, self.gk = 1 + 0.2 * randn(seed + 5, D).float(), (1 + 0.2 * randn(seed + 6, D)).bfloat16()
+        self.qk = vsa.QKNormRope(self.rope, self.gq, self.gk, EPS)
+
+    def block(self, training):
+        return vsa.AttentionBlock(self.plan, self.B, self.H, self.D, self.C, self.keep, self.qk, training=training)
+
+    def run(self, block):
+        out = block.forward(self.x, self.w_in, self.w_out, self.b_in, self.b_out)
+        vsa.vsa_sync_status(self.plan)
+        return out
+
+    def turned(self, q, gain):
+        return BO.rotate(BO.head_norm(q, gain, EPS), self.ang, self.halves)
+
+    def forward64(self, x, kept):
+        """The whole block in fp64 under a given selection."""
+        y = BO.heads(BO.linear(x, self.w_in, self.b_in), 4 * self.H)
+        q, k, v, g = np.split(y, 4, axis=1)
+        f = O.layer(self.turned(q, self.gq), self.turned(k, self.gk), v, g, self.p, self.keep, kept=kept)
+        return BO.linear(f["out"], self.w_out, self.b_out) + x
+
+
+ARGS = [
+    ((40, 70), (4, 8, 8), (4, 4, 4), 1, 2, 64, 96, (24, 20, 20), False, 2, 100),
+    ((5, 0, 64, 65), (5, 6, 7), (4, 4, 4), 2, 2, 128, 200, (44, 42, 42), True, 3, 200),
+    ((130,), (8, 9, 9), (4, 8, 4), 1, 3, 128, 136, (44, 42, 42), False, 2, 300),
+]
+cases = pytest.mark.parametrize("args", ARGS, ids=["d64", "ragged_b2", "r128"])
+
+
+@cases
+def test_block_forward(args):
+    c = Case(*args)
+    H = c.H
+    train, infer = c.block(True), c.block(False)
+    out, out_i = c.run(train), c.run(infer)
+    # the products' heads: one rounding and the fp32 sum
+    want = BO.linear(c.x, c.w_in, c.b_in)
+    slack = dot_slack(f64(c.x), f64(c.w_in)) + 2.0 ** -23 * np.abs(want)
+    close(train.qkvg, BO.heads(want, 4 * H), BO.heads(slack, 4 * H), "qkvg")
+    assert torch.equal(infer.qkv, train.qkvg[:, :3 * H]) and torch.equal(infer.g, train.qkvg[:, 3 * H:])
+    q, k, v, g = train.qkvg.split(H, 1)
+    lay = train.layer
+    for got, src, gain in ((lay.q_t, q, c.gq), (lay.k_t, k, c.gk)):
+        z = BO.head_norm(src, gain, EPS)
+        big = np.abs(z).max(-1, keepdims=True)
+        close(vsa.vsa_unpermute(c.plan, got), c.turned(src, gain), (c.D / 2 + 24) * 2.0 ** -24 * big, "q_t, k_t")
+    assert torch.equal(lay.v_t, vsa.vsa_permute(c.plan, v.contiguous()))
+    assert torch.equal(lay.g_t, vsa.vsa_permute(c.plan, g.contiguous()))
+    for b, name in ((train, "training"), (infer, "fused")):
+        lay = b.layer
+        kept = lay.topk_idx.cpu().numpy().astype(np.int64)
+        qn, kn = (vsa.vsa_unpermute(c.plan, t) for t in (lay.q_t, lay.k_t))
+        ref = O.layer(qn, kn, v, g, c.p, c.keep, kept=kept)
+        assert_close(f64(lay.out), ref["out"], what=name)
+        want = BO.linear(lay.out, c.w_out, c.b_out) + f64(c.x)
+        close(b.out, want, dot_slack(BO.rows(lay.out), f64(c.w_out)) + 2.0 ** -22 * np.abs(want), name)
+    assert out.data_ptr() == train.out.data_ptr() and out_i.shape == c.x.shape
+
+
+@cases
+def test_block_backward(args):
+    c = Case(*args)
+    H = c.H
+    block = c.block(True)
+    c.run(block)
+    d_out = randn(args[-1] + 9, *c.x.shape)
+    dx, dw_in, db_in, dw_out, db_out, dgq, dgk = block.backward(d_out)
+    vsa.vsa_sync_status(c.plan)
+    lay = block.layer
+    M = c.B * c.N
+    # the output product
+    wd, ww, wb = BO.linear_backward(d_out, lay.out, c.w_out)
+    g, o = f64(d_out).reshape(M, -1), BO.rows(lay.out).reshape(M, -1)
+    close(block.d_o, BO.heads(wd, H), BO.heads(dot_slack(f64(d_out), f64(c.w_out).T), H), "d_o")
+    close(dw_out, ww, dot_slack(g.T, o.T), "dw_out")
+    close(db_out, wb, M * 2.0 ** -24 * np.abs(g).sum(0) + 1e-30, "db_out", half_step=0.0)
+    # the layer, and the norm and rotation under it: the layer's own bounds (2e-2 of the largest, 4e-3
+    # of the mean), with the norm's projection of the gradient and one more rounding on top
+    kept = lay.topk_idx.cpu().numpy().astype(np.int64)
+    q, k, v, gt = block.qkvg.split(H, 1)
+    qn, kn = (vsa.vsa_unpermute(c.plan, t) for t in (lay.q_t, lay.k_t))
+    fwd = O.layer(qn, kn, v, gt, c.p, c.keep, kept=kept)
+    bwd = O.layer_backward(block.d_o, fwd, c.p)
+    got = block.d_qkvg.split(H, 1)
+    for i, (src, gain, name, dg) in enumerate(((q, c.gq, "dq", dgq), (k, c.gk, "dk", dgk))):
+        want, want_g = BO.head_norm_backward(BO.rotate(bwd[name], c.ang, c.halves, inverse=True), src, gain, EPS)
+        assert_rel(f64(got[i]), want, 3e-2, 8e-3, what=name)
+        assert_rel(f64(dg), want_g, 3e-2, 2e-2, what=name + " gain")
+    assert_rel(f64(got[2]), bwd["dv"], what="dv")
+    assert_rel(f64(got[3]), bwd["dg"], what="dg")
+    # the input product, with the residual's gradient added
+    wd, ww, wb = BO.linear_backward(block.d_qkvg, c.x, c.w_in)
+    g = BO.rows(block.d_qkvg)
+    wd = wd + f64(d_out)
+    close(dx, wd, dot_slack(g, f64(c.w_in).T) + 2.0 ** -23 * np.abs(wd), "dx")
+    close(dw_in, ww, dot_slack(g.reshape(M, -1).T, f64(c.x).reshape(M, -1).T), "dw_in")
+    close(db_in, wb, M * 2.0 ** -24 * np.abs(g).sum((0, 1)) + 1e-30, "db_in", half_step=0.0)
+
+
+def test_block_gradient_against_differences():
+    """<dx, d> of the whole block against central differences of the fp64 forward along d (the
+    selection held).  Some dozen roundings of 2^-9 stand between them: within 5 % of |dx| for a
+    normal d, whose product with dx is of the size |dx| itself."""
+    c = Case(*ARGS[0])
+    block = c.block(True)
+    c.run(block)
+    kept = block.layer.topk_idx.cpu().numpy().astype(np.int64)
+    d_out = randn(109, *c.x.shape)
+    dx = f64(block.backward(d_out)[0])
+    rng = np.random.default_rng(1)
+    x, w = f64(c.x), f64(d_out)
+    for _ in range(3):
+        d = rng.normal(size=x.shape)
+        h = 1e-4
+        diff = (w * (c.forward64(x + h * d, kept) - c.forward64(x - h * d, kept))).sum() / (2 * h)
+        assert abs(diff - (dx * d).sum()) <= 0.05 * np.sqrt((dx * dx).sum())
+
+
+def test_layer_with_norm_and_rotation_is_the_composition():
+    """Layer(qk=...) feeds the same tiles to the attention as vsa_norm_rope before a plain layer."""
+    c = Case(*ARGS[1])
+    q, k, v, g = (randn(s, c.B, c.H, c.N, c.D) for s in (1, 2, 3, 4))
+    keep = c.plan.n_video_tiles                                  # no selection to differ in
+    a = vsa.Layer(c.plan, c.B, c.H, c.D, keep, qk=c.qk)
+    b = vsa.Layer(c.plan, c.B, c.H, c.D, keep)
+    u = vsa.Layer(c.plan, c.B, c.H, c.D, keep, qk=c.qk, fused=False)
+    qn, kn = vsa.vsa_norm_rope(c.plan, [vsa.HeadTensor(q, c.gq), vsa.HeadTensor(k, c.gk)], c.rope, EPS)
+    out_a, out_b, out_u = a(q, k, v, g), b(qn, kn, v, g), u(q, k, v, g)
+    vsa.vsa_sync_status(c.plan)
+    for name in ("q_t", "k_t", "v_t"):
+        assert torch.equal(getattr(a, name), getattr(b, name))
+        assert torch.equal(getattr(u, name), getattr(b, name))
+    ref = O.layer(qn, kn, v, g, c.p, keep)
+    for out in (out_a, out_b, out_u):
+        assert_close(f64(out), ref["out"], what="layer")
+
+
+def test_streams_and_graphs():
+    """On another stream, captured and replayed on new inputs, and two linears at once on two streams
+    with a plan between them: the results of the plain calls, to the bit."""
+    c = Case(*ARGS[0])
+    block = c.block(False)
+    want = c.run(block).clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = block.forward(c.x, c.w_in, c.w_out, c.b_in, c.b_out, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    train = c.block(True)
+    c.run(train)
+    d_out = randn(7, *c.x.shape)
+    grads = [t.clone() for t in train.backward(d_out)]
+    x2 = c.x.clone()
+    for step in (lambda: train.forward(x2, c.w_in, c.w_out, c.b_in, c.b_out), lambda: train.backward(d_out)):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        train.forward(x2, c.w_in, c.w_out, c.b_in, c.b_out)
+        outs = train.backward(d_out)
+    x2.copy_(randn(8, *c.x.shape))
+    graph.replay()
+    x2.copy_(c.x)
+    graph.replay()
+    torch.cuda.synchronize()
+    vsa.vsa_sync_status(c.plan)
+    assert all(torch.equal(a, b) for a, b in zip(outs, grads))
+    # two at once
+    xs = [randn(20 + i, 1, 3000, 512) for i in range(2)]
+    w, b = randn(30, 1024, 512, scale=0.05), randn(31, 1024)
+    wants = [vsa.vsa_linear(c.plan, x, w, b, act="silu") for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    ys = []
+    for _ in range(5):
+        ys = [vsa.vsa_linear(c.plan, x, w, b, act="silu", stream=st) for x, st in zip(xs, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, t) for y, t in zip(ys, wants))
+    vsa.vsa_sync_status(c.plan)
+
+
+def test_repeats_are_bitwise_equal():
+    """Sums are taken in a fixed order: two runs give the same bits, the gains' and biases' gradients
+    among them, and in split products."""
+    c = Case(*ARGS[2])
+    block = c.block(True)
+    d_out = randn(9, *c.x.shape)
+    runs = []
+    for _ in range(2):
+        c.run(block)
+        runs.append([block.out.clone(), *(t.clone() for t in block.backward(d_out))])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+    x, w = randn(1, 1, 40, 4096), randn(2, 256, 4096, scale=0.02)
+    assert torch.equal(vsa.vsa_linear(c.plan, x, w), vsa.vsa_linear(c.plan, x, w))

@@ -347,7 +347,7 @@ static vsa_status norm_rope_forward(vsa_plan p, vsa_rope rope, const vsa_head_te
     VSA_TRY(check_view(s.x, B, H, p->n_tokens, D, false, 0, "x"));
     if (tiled) {
       VSA_TRY(check_ptr(s.y.ptr, "y"));
-      VSA_TRY(check_ptr(s.pooled, "pooled"));
+      if (s.pooled != nullptr) VSA_TRY(check_ptr(s.pooled, "pooled"));
       if (s.y.ptr == s.x.ptr) return fail(VSA_ERR_INVALID_ARG, "the permute is not done in place");
     } else {
       VSA_TRY(check_view(s.y, B, H, p->n_tokens, D, true, 8, "y"));
@@ -524,6 +524,12 @@ vsa_status vsa_linear_backward(vsa_plan p, const vsa_linear_grad_args* q, void* 
       if (q->x_pre.ptr != nullptr) {
         VSA_TRY(check_linear_view(q->x_pre, q->B, q->N, q->x_heads, q->C, false, "x_pre"));
         VSA_TRY(check_in_place(q->dx, q->x_pre, q->B, q->x_heads, q->N, "dx"));
+      }
+      if (q->dx_add.ptr != nullptr) {
+        if (q->x_pre.ptr != nullptr)
+          return fail(VSA_ERR_INVALID_ARG, "dx_add does not go with x_pre");
+        VSA_TRY(check_linear_view(q->dx_add, q->B, q->N, q->x_heads, q->C, false, "dx_add"));
+        VSA_TRY(check_in_place(q->dx, q->dx_add, q->B, q->x_heads, q->N, "dx"));
       }
     }
     if (q->dw != nullptr) {

@@ -89,6 +89,7 @@ struct GemmArgs {
   OutView y, res, pre;
   const void* bias;
   int bias_f32, act;
+  int add;                         // dgrad: res is added, and not the pre-activation
   float* partial;                  // fp32 [splits][tiles - whole][256][bn]
 };
 
@@ -641,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float2 x[16];
 #pragma unroll
           for (int e = 0; e < 4; ++e) unpack(x4[e], &x[4 * e]);
-          if (kOrder == kForward) {
+          if (kOrder == kForward || a.add) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) f[e] = add2(f[e], x[e]);
           } else {
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(256) split_join_kernel(const __grid_constant__
   if (kOrder != kWgrad && a.res.ptr != nullptr) {
     float2 x[4];
     unpack(*at(a.res), x);
-    if (kOrder == kForward) {
+    if (kOrder == kForward || a.add) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[e] = add2(f[e], x[e]);
     } else {
@@ -1156,7 +1157,8 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.partial = static_cast<float*>(ws);
     a.Nrow = q.N;
     a.y = out_view(q.dx, q.x_heads, q.C);
-    a.res = out_view(q.x_pre, q.x_heads, q.C);
+    a.add = q.dx_add.ptr != nullptr;
+    a.res = out_view(a.add ? q.dx_add : q.x_pre, q.x_heads, q.C);
     a.act = q.x_act;
     const vsa_status st = launch<kDgrad>(p, g, 128, matrix(q.w, q.O, q.C), kBK, a,
                                          int64_t(q.O) * q.C * 2, stream);

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, kTiled ? 2 : 4)
         }
       }
       y += y_head;
-      if (kTiled) {
+      if (kTiled && t.pooled != nullptr) {
 #pragma unroll
         for (int off = kCpr; off < 32; off <<= 1)
 #pragma unroll
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, kTiled ? 2 : 4)
       }
     }
   }
-  if (kTiled) {
+  if (kTiled && t.pooled != nullptr) {
     // the tile's means: the warps' sums, a head after the other
     __syncthreads();
     const float inv = 1.0f / float(n);

@@ -71,7 +71,7 @@ _VIEW = struct.Struct("@Pqqq")
 _HEAD_TENSOR = struct.Struct("@PqqqPiiiPqqqP")
 _HEAD_GRAD = struct.Struct("@PqqqPqqqPiiiPqqqP")
 _LINEAR = struct.Struct("@iiiiiqPqqqPPiiPqqqPqqqPqqq")
-_LINEAR_GRAD = struct.Struct("@iiiiiqPqqqPqqqPPqqqiPqqqPP")
+_LINEAR_GRAD = struct.Struct("@iiiiiqPqqqPqqqPPqqqiPqqqPPPqqq")
 
 
 class _RopeDesc(ctypes.Structure):
@@ -86,7 +86,7 @@ _VIEW = struct.Struct("@Pqqq")
 _HEAD_TENSOR = struct.Struct("@PqqqPiiiPqqqP")
 _HEAD_GRAD = struct.Struct("@PqqqPqqqPiiiPqqqP")
 _LINEAR = struct.Struct("@iiiiiqPqqqPPiiPqqqPqqqPqqq")
-_LINEAR_GRAD = struct.Struct("@iiiiiqPqqqPqqqPPqqqiPqqqPP")
+_LINEAR_GRAD = struct.Struct("@iiiiiqPqqqPqqqPPqqqiPqqqPPPqqq")
 
 
 def lib():
@@ -774,7 +774,8 @@ def vsa_rope_apply(plan: Plan, rope: Rope, x: torch.Tensor, y: Optional[torch.Te
 
 class HeadTensor(NamedTuple):
     """One tensor of vsa_norm_rope: x [B,H,N,D] (any strides), its gain [D] (bf16 or
-    fp32; None: 1), what is done to it, and where the result goes (None: new)."""
+    fp32; None: 1), what is done to it, and where the result goes (None: new;
+    ``pooled=False``: no tile means)."""
     x: torch.Tensor
     gain: Optional[torch.Tensor] = None
     norm: bool = True
@@ -808,7 +809,7 @@ def _norm_rope(plan, items, rope, eps, tiled, stream):
         gv, gt = _vector(plan, gain, "gain", D)
         if tiled:
             y = out(tiles) if y is None else y
-            pooled = out(means, _F32) if pooled is None else pooled
+            pooled = out(means, _F32) if pooled is None else (None if pooled is False else pooled)
             yv = (_dense(plan, y, "y", _BF16, tiles), 0, 0, 0)
             pv = _dense(plan, pooled, "pooled", _F32, means)
             res.append((y, pooled))
@@ -937,10 +938,11 @@ def vsa_linear_backward(plan: Plan, dy: torch.Tensor, x: torch.Tensor, w: torch.
                         x_pre: Optional[torch.Tensor] = None, x_act: str = "identity",
                         dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
                         db: Optional[torch.Tensor] = None, need=(True, True, True),
-                        ws: Optional[torch.Tensor] = None, stream=None):
+                        dx_add: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                        stream=None):
     """Gradients of x w^T + bias under dy: (dx, dw bf16 [O,C], db fp32 [O]); ``need`` leaves
     some of them out (None).  With ``x_pre`` (x = x_act(x_pre)) dx is the gradient of
-    x_pre."""
+    x_pre; ``dx_add`` is added to dx (what reaches x by another way; not with x_pre)."""
     B, N, xh, C = _sides(x, "x")
     _, _, yh, O = _sides(dy, "dy")
     out = _Out(plan, stream)
@@ -954,7 +956,8 @@ def vsa_linear_backward(plan: Plan, dy: torch.Tensor, x: torch.Tensor, w: torch.
     db = (out((O,), _F32) if db is None else db) if need[2] else None
     args = _LINEAR_GRAD.pack(B, xh, C, yh, O, N, *dyv, *xv, _dense(plan, w, "w", _BF16, (O, C)), *xpv, act,
                              *_view(plan, dx, "dx", x.shape), _dense(plan, dw, "dw", _BF16, (O, C)),
-                             _dense(plan, db, "db", _F32, (O,)))
+                             _dense(plan, db, "db", _F32, (O,)),
+                             *_view(plan, dx_add if need[0] else None, "dx_add", x.shape))
     if ws is None:
         ws = out((max(_workspace_bytes(plan, "vsa_linear_backward_workspace_size", B, N, C, O), 16),), _U8)
     _check(lib().vsa_linear_backward(plan.handle, args, ws.data_ptr(), ws.numel() * ws.element_size(),
@@ -973,6 +976,25 @@ def vsa_act_backward(plan: Plan, dy: torch.Tensor, pre: torch.Tensor, act: str,
     return out
 
 
+class QKNormRope(NamedTuple):
+    """What a layer does to its queries and keys on their way in: RMS norm of every
+    head with the gains [D] (bf16 or fp32; None: 1; ``norm=False``: none) and the rotation
+    (``rope=None``: none).  Q, K and V then go into tile order in one launch
+    (vsa_norm_rope_permute_pool) and may be strided, views of one projection for
+    instance."""
+    rope: Optional[Rope] = None
+    q_gain: Optional[torch.Tensor] = None
+    k_gain: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+    norm: bool = True
+
+    def items(self, q, k, v, tiles, means):
+        turn = self.rope is not None
+        return [HeadTensor(q, self.q_gain, self.norm, turn, tiles[0], means[0]),
+                HeadTensor(k, self.k_gain, self.norm, turn, tiles[1], means[1]),
+                HeadTensor(v, None, False, False, tiles[2], means[2])]
+
+
 class Layer:
     """The five steps in sequence on caller-visible buffers, all launches on
     one stream.  ``fused=True`` (default): permute Q, K, V with the tile means
@@ -980,11 +1002,14 @@ class Layer:
     the gated combine fused into its epilogue, writing natural order (the gate
     is read in natural order): 5 launches.  ``fused=False``: the unfused chain
     (permute Q, K, V, G; pool + coarse + top-k; attention; combine).  Buffers
-    are allocated once and reused by every call."""
+    are allocated once and reused by every call.  ``qk`` (a QKNormRope): Q and K are
+    normed and rotated in the permuting pass, 3 launches in all when fused."""
 
     def __init__(self, plan: Plan, B: int, H: int, D: int, k: int, scale: Optional[float] = None,
-                 device=None, fused: bool = True, k_ref: Optional[int] = None):
+                 device=None, fused: bool = True, k_ref: Optional[int] = None,
+                 qk: Optional[QKNormRope] = None):
         self.plan, self.B, self.H, self.D, self.k, self.fused = plan, B, H, D, k, fused
+        self.qk = qk
         # k_ref: reference tiles each video query tile keeps (None: all of them)
         self.k_ref = k_ref
         self.scale = D ** -0.5 if scale is None else float(scale)
@@ -1005,9 +1030,14 @@ class Layer:
         p = self.plan
         if self.fused:
             qbar, kbar, vbar = pooled_slots(p, self.ws, self.B, self.H, self.D)
-            vsa_permute_pool(p, q, self.q_t, qbar, stream)
-            vsa_permute_pool(p, k, self.k_t, kbar, stream)
-            vsa_permute_pool(p, v, self.v_t, vbar, stream)
+            if self.qk is not None:
+                vsa_norm_rope_permute_pool(p, self.qk.items(q, k, v, (self.q_t, self.k_t, self.v_t),
+                                                            (qbar, kbar, vbar)),
+                                           self.qk.rope, self.qk.eps, stream)
+            else:
+                vsa_permute_pool(p, q, self.q_t, qbar, stream)
+                vsa_permute_pool(p, k, self.k_t, kbar, stream)
+                vsa_permute_pool(p, v, self.v_t, vbar, stream)
             vsa_coarse_topk_pooled(p, self.B, self.H, self.D, self.k, self.ws, self.scale,
                                    o_coarse=self.o_coarse, topk_idx=self.topk_idx, stream=stream)
             if self.k_ref is not None:
@@ -1020,9 +1050,13 @@ class Layer:
             vsa_sparse_attn_combine(p, self.q_t, self.k_t, self.v_t, self.topk_idx, self.k, g,
                                     self.o_coarse, self.scale, out=self.out, stream=stream)
             return self.out
-        vsa_permute(p, q, self.q_t, stream)
-        vsa_permute(p, k, self.k_t, stream)
-        vsa_permute(p, v, self.v_t, stream)
+        if self.qk is not None:
+            vsa_norm_rope_permute_pool(p, self.qk.items(q, k, v, (self.q_t, self.k_t, self.v_t), (False,) * 3),
+                                       self.qk.rope, self.qk.eps, stream)
+        else:
+            vsa_permute(p, q, self.q_t, stream)
+            vsa_permute(p, k, self.k_t, stream)
+            vsa_permute(p, v, self.v_t, stream)
         vsa_coarse_topk(p, self.q_t, self.k_t, self.v_t, self.k, self.scale, ws=self.ws,
                         o_coarse=self.o_coarse, topk_idx=self.topk_idx, stream=stream)
         vsa_permute(p, g, self.g_t, stream)
@@ -1102,11 +1136,21 @@ class TrainingLayer:
     ``backward(d_out)`` returns (dq, dk, dv, dg) in natural order [B,H,N,D],
     bf16: permute d_out, combine backward, coarse backward, attention backward
     (with the pooling term), and four unpermutes.  The selection passes no
-    gradient.  Buffers are allocated once and reused."""
+    gradient.  Buffers are allocated once and reused.
+
+    ``qk`` (a QKNormRope): Q and K are normed and rotated, and Q, K, V and the gate (all of
+    them may be strided) go into tile order in one launch; the backward comes out
+    through vsa_norm_rope_backward, which needs the forward's q and k unchanged and leaves the
+    gains' gradients in ``d_gains`` (fp32 [D] each, or None)."""
 
     def __init__(self, plan: Plan, B: int, H: int, D: int, k: int, scale: Optional[float] = None,
-                 device=None, k_ref: Optional[int] = None):
+                 device=None, k_ref: Optional[int] = None, qk: Optional[QKNormRope] = None):
         self.plan, self.B, self.H, self.D, self.k, self.k_ref = plan, B, H, D, k, k_ref
+        self.qk, self.d_gains = qk, (None, None)
+        if qk is not None:
+            self.nws = norm_rope_backward_workspace(plan, 4, D)
+            self.d_gains = tuple(None if g is None else torch.empty(D, dtype=torch.float32, device=g.device)
+                                 for g in (qk.q_gain, qk.k_gain))
         self.scale = D ** -0.5 if scale is None else float(scale)
         dev = torch.device("cuda", plan.device) if device is None else torch.device(device)
         tiled = (B, H, plan.n_padded, D)
@@ -1132,12 +1176,18 @@ class TrainingLayer:
     def forward(self, q, k, v, g, stream=None):
         p = self.plan
         qbar, kbar, vbar = pooled_slots(p, self.ws, self.B, self.H, self.D)
-        vsa_permute_pool(p, q, self.q_t, qbar, stream)
-        vsa_permute_pool(p, k, self.k_t, kbar, stream)
-        vsa_permute_pool(p, v, self.v_t, vbar, stream)
+        if self.qk is not None:
+            self._inputs = (q, k)
+            vsa_norm_rope_permute_pool(
+                p, [*self.qk.items(q, k, v, (self.q_t, self.k_t, self.v_t), (qbar, kbar, vbar)),
+                    HeadTensor(g, None, False, False, self.g_t, False)], self.qk.rope, self.qk.eps, stream)
+        else:
+            vsa_permute_pool(p, q, self.q_t, qbar, stream)
+            vsa_permute_pool(p, k, self.k_t, kbar, stream)
+            vsa_permute_pool(p, v, self.v_t, vbar, stream)
+            vsa_permute(p, g, self.g_t, stream)
         vsa_coarse_topk_pooled(p, self.B, self.H, self.D, self.k, self.ws, self.scale,
                                o_coarse=self.o_coarse, topk_idx=self.topk_idx, stream=stream)
-        vsa_permute(p, g, self.g_t, stream)
         kr = p.n_prefix_tiles if self.k_ref is None else self.k_ref
         if self.k_ref is not None:
             vsa_select_reference(p, self.B, self.H, self.D, self.k_ref, self.ws, self.scale,
@@ -1152,8 +1202,10 @@ class TrainingLayer:
                          stream=stream)
         return self.out
 
-    def backward(self, d_out, stream=None):
+    def backward(self, d_out, stream=None, out=None):
+        """(dq, dk, dv, dg); ``out``: four tensors for them (with ``qk`` they may be strided)."""
         p = self.plan
+        grads = self.grads if out is None else out
         vsa_permute(p, d_out, self.d_out_t, stream)
         vsa_combine_backward(p, self.d_out_t, self.o_fine_t, self.g_t, self.o_coarse, self.delta,
                              self.dg_t, self.d_o_coarse, stream)
@@ -1164,6 +1216,74 @@ class TrainingLayer:
                                  self.k, self.lse, self.delta, self.bws, topk_ref=self.topk_ref,
                                  k_ref=self.k_ref, d_bar=self.d_bar, scale=self.scale,
                                  out=(self.dq_t, self.dk_t, self.dv_t), stream=stream)
-        for src, dst in zip((self.dq_t, self.dk_t, self.dv_t, self.dg_t), self.grads):
+        if self.qk is not None:
+            (q, k), c, turn = self._inputs, self.qk, self.qk.rope is not None
+            vsa_norm_rope_backward(
+                p, [HeadGrad(self.dq_t, q, c.q_gain, c.norm, turn, grads[0], self.d_gains[0]),
+                    HeadGrad(self.dk_t, k, c.k_gain, c.norm, turn, grads[1], self.d_gains[1]),
+                    HeadGrad(self.dv_t, None, None, False, False, grads[2]),
+                    HeadGrad(self.dg_t, None, None, False, False, grads[3])], c.rope, c.eps, tiled=True,
+                ws=self.nws, stream=stream)
+            return grads
+        for src, dst in zip((self.dq_t, self.dk_t, self.dv_t, self.dg_t), grads):
             vsa_unpermute(p, src, dst, stream)
-        return self.grads
+        return grads
+
+
+class AttentionBlock:
+    """The attention half of a transformer block on rows x [B,N,C] in natural token order:
+
+        q, k, v, g = heads of x w_in^T + b_in        (w_in [4 H D, C], in this order)
+        out = x + layer(q, k, v, g) w_out^T + b_out  (w_out [C, H D])
+
+    with the layer's norm and rotation of Q and K (``qk``).  Biases may be None.  Forward
+    only: two products (Q, K, V; the gate), the fused Layer, and the output product with bias
+    and residual in its epilogue, 6 launches for as many rows as fill the GPU.  ``training``: one
+    product for all four, TrainingLayer, and ``backward(d_out)``, which returns the gradients
+    (dx, dw_in, db_in, dw_out, db_out, dq_gain, dk_gain); x and the weights must be as they were in
+    the forward.  Buffers are allocated once and reused."""
+
+    def __init__(self, plan: Plan, B: int, H: int, D: int, C: int, k: int, qk: Optional[QKNormRope] = None,
+                 scale: Optional[float] = None, k_ref: Optional[int] = None, training: bool = False):
+        self.plan, self.B, self.H, self.D, self.C, self.training = plan, B, H, D, C, training
+        dev, N = torch.device("cuda", plan.device), plan.n_tokens
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        qk = QKNormRope(norm=False) if qk is None else qk
+        self.layer = (TrainingLayer if training else Layer)(plan, B, H, D, k, scale, k_ref=k_ref, qk=qk)
+        self.out = torch.empty(B, N, C, **bf)
+        need = [_workspace_bytes(plan, "vsa_linear_workspace_size", B, N, C, n * H * D) for n in (1, 3, 4)]
+        need.append(_workspace_bytes(plan, "vsa_linear_workspace_size", B, N, H * D, C))
+        if training:
+            self.qkvg = torch.empty(B, 4 * H, N, D, **bf)
+            self.d_qkvg, self.d_o = torch.empty_like(self.qkvg), torch.empty(B, H, N, D, **bf)
+            self.dx = torch.empty(B, N, C, **bf)
+            self.dw_in, self.dw_out = torch.empty(4 * H * D, C, **bf), torch.empty(C, H * D, **bf)
+            self.db_in = torch.empty(4 * H * D, dtype=torch.float32, device=dev)
+            self.db_out = torch.empty(C, dtype=torch.float32, device=dev)
+            need.append(_workspace_bytes(plan, "vsa_linear_backward_workspace_size", B, N, C, 4 * H * D))
+            need.append(_workspace_bytes(plan, "vsa_linear_backward_workspace_size", B, N, H * D, C))
+        else:
+            self.qkv, self.g = torch.empty(B, 3 * H, N, D, **bf), torch.empty(B, H, N, D, **bf)
+        self.ws = torch.empty(max(*need, 16), dtype=torch.uint8, device=dev)
+
+    def forward(self, x, w_in, w_out, b_in=None, b_out=None, stream=None):
+        p, H, n = self.plan, self.H, 3 * self.H * self.D
+        if self.training:
+            self._saved = (x, w_in, w_out)
+            vsa_linear(p, x, w_in, b_in, y=self.qkvg, ws=self.ws, stream=stream)
+            o = self.layer.forward(*self.qkvg.split(H, 1), stream=stream)
+        else:
+            vsa_linear(p, x, w_in[:n], None if b_in is None else b_in[:n], y=self.qkv, ws=self.ws, stream=stream)
+            vsa_linear(p, x, w_in[n:], None if b_in is None else b_in[n:], y=self.g, ws=self.ws, stream=stream)
+            o = self.layer(*self.qkv.split(H, 1), self.g, stream=stream)
+        return vsa_linear(p, o, w_out, b_out, residual=x, y=self.out, ws=self.ws, stream=stream)
+
+    def backward(self, d_out, stream=None):
+        p = self.plan
+        x, w_in, w_out = self._saved
+        vsa_linear_backward(p, d_out, self.layer.out, w_out, dx=self.d_o, dw=self.dw_out, db=self.db_out,
+                            ws=self.ws, stream=stream)
+        self.layer.backward(self.d_o, stream, out=self.d_qkvg.split(self.H, 1))
+        vsa_linear_backward(p, self.d_qkvg, x, w_in, dx=self.dx, dw=self.dw_in, db=self.db_in, dx_add=d_out,
+                            ws=self.ws, stream=stream)
+        return (self.dx, self.dw_in, self.db_in, self.dw_out, self.db_out, *self.layer.d_gains)
