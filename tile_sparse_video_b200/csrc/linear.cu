@@ -274,6 +274,11 @@ __device__ __forceinline__ int64_t col_offset(const OutView& v, int col) {
   return h * v.sh + (col - (h << v.shift));
 }
 
+// Programmatic launch: the kernel that joins partial sums is put on the GPU while the one that
+// writes them still runs (which says so at its start), and waits here for its end.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // An epilogue warp's 32 x 64 bytes of shared memory: 16-byte chunk q of row r at chunk q ^ (r/2 & 3),
 // so that neither a lane per row nor four lanes per row meet in a bank.
 __device__ __forceinline__ uint4* chunk_at(uint8_t* staging, int r, int q) {
@@ -302,6 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int items = a.whole + (a.m_tiles * a.n_tiles - a.whole) * a.splits;
 
+  let_next_start();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full + 8 * s, 1);      // the leader's: its producer, and both CTAs' bytes
@@ -679,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // eight of 16 rows): the order of C within 32 columns does not matter to a sum, so lane t's eight
 // neighbours stand for the pairs 2t, 2t + 1, 2t + 8, 2t + 9 of two products.  The warps'
 // fp32 sums meet in shared memory, in warp order.
-constexpr int kFewThreads = 256, kFewUnroll = 4, kFewRows = 8;
+constexpr int kFewThreads = 256, kFewRows = 8;
 
 struct FewArgs {
   const uint16_t *x, *w;
@@ -726,8 +732,8 @@ __device__ __forceinline__ void finish(const FewArgs& a, int r, int o, float2 (&
   *at(a.y) = pack_bf16(f[0].x, f[0].y);
 }
 
-// A piece of w, read once: volatile, so that the loads of a step stay ahead of its products.
-__device__ __forceinline__ uint4 load_w(const uint16_t* p, bool live) {
+// 16 bytes that are read once: volatile, so that the loads of a step stay ahead of its arithmetic.
+__device__ __forceinline__ uint4 load_once(const uint16_t* p, bool live) {
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
   if (live)
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -736,7 +742,9 @@ __device__ __forceinline__ uint4 load_w(const uint16_t* p, bool live) {
   return v;
 }
 
-__global__ void __launch_bounds__(kFewThreads, 4) linear_few_kernel(const __grid_constant__ FewArgs a) {
+// kPieces 16-byte pieces of w in flight a lane and step, kPerSm blocks an SM.
+template <int kPieces, int kPerSm>
+__global__ void __launch_bounds__(kFewThreads, kPerSm) linear_few_kernel(const __grid_constant__ FewArgs a) {
   constexpr int kWarps = kFewThreads / 32, kStep = kWarps * 32;
   __shared__ float sum[kWarps][8][8 + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -748,20 +756,20 @@ __global__ void __launch_bounds__(kFewThreads, 4) linear_few_kernel(const __grid
   const uint16_t* x = a.x + bx * a.xb + int64_t(g - bx * a.N) * a.xn;
   float acc[2] = {0.0f, 0.0f};
   const int first = warp * 32 + 8 * t;
-  uint4 next[kFewUnroll];                            // the step's pieces of w, a step ahead
+  uint4 next[kPieces];                            // the step's pieces of w, a step ahead
 #pragma unroll
-  for (int i = 0; i < kFewUnroll; ++i) next[i] = load_w(w + first + i * kStep, first + i * kStep < a.C);
-  for (int k0 = first; k0 - 8 * t < a.C; k0 += kStep * kFewUnroll) {
-    uint4 u[kFewUnroll], v[kFewUnroll];
+  for (int i = 0; i < kPieces; ++i) next[i] = load_once(w + first + i * kStep, first + i * kStep < a.C);
+  for (int k0 = first; k0 - 8 * t < a.C; k0 += kStep * kPieces) {
+    uint4 u[kPieces], v[kPieces];
 #pragma unroll
-    for (int i = 0; i < kFewUnroll; ++i) {
-      const int k = k0 + i * kStep, h = k >> a.x_shift, kn = k + kStep * kFewUnroll;
+    for (int i = 0; i < kPieces; ++i) {
+      const int k = k0 + i * kStep, h = k >> a.x_shift, kn = k + kStep * kPieces;
       u[i] = next[i];
       v[i] = load_or_zero(x + h * a.xh + (k - (h << a.x_shift)), live && k < a.C);
-      next[i] = load_w(w + kn, kn < a.C);
+      next[i] = load_once(w + kn, kn < a.C);
     }
 #pragma unroll
-    for (int i = 0; i < kFewUnroll; ++i) {
+    for (int i = 0; i < kPieces; ++i) {
       mma_8x8(acc, v[i].x, v[i].y, u[i].x, u[i].y);
       mma_8x8(acc, v[i].z, v[i].w, u[i].z, u[i].w);
     }
@@ -784,6 +792,7 @@ __global__ void __launch_bounds__(kFewThreads, 4) linear_few_kernel(const __grid
 // would have done follows.  A thread takes eight columns of a row, a block 2,048 elements of a tile.
 template <int kOrder>
 __global__ void __launch_bounds__(256) split_join_kernel(const __grid_constant__ GemmArgs a) {
+  wait_for_last();
   const int octs = a.bn / 8, per_block = 256 / octs;       // rows of a block
   const int i = blockIdx.x / (kBM / per_block), part = blockIdx.x % (kBM / per_block);
   const int in_tile = part * per_block + threadIdx.x / octs, in_row = (threadIdx.x % octs) * 8;
@@ -850,6 +859,7 @@ constexpr int kColsumRows = 64;
 __global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, const Div by_nrow, int M, int O,
                                                      int rows_per, float* part) {
   __shared__ float s[8][256];
+  let_next_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 256 + 8 * lane;
   float2 acc[4] = {};
@@ -861,8 +871,11 @@ __global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, const Div
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t ri = r + 8 * i, b = ri / by_nrow;
-        v[i] = load_or_zero(base + b * dy.sb + (ri - b * by_nrow.d) * dy.sn, int(ri) < r1);
+        v[i] = load_once(base + b * dy.sb + (ri - b * by_nrow.d) * dy.sn, int(ri) < r1);
       }
+      // nothing is added before all eight are asked for
+      asm volatile("" : "+r"(v[0].x), "+r"(v[1].x), "+r"(v[2].x), "+r"(v[3].x), "+r"(v[4].x), "+r"(v[5].x),
+                        "+r"(v[6].x), "+r"(v[7].x));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float2 f[4];
@@ -886,6 +899,7 @@ __global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, const Div
 
 __global__ void __launch_bounds__(1024) colsum_join_kernel(const float* part, int runs, int O, float* db) {
   __shared__ float s[32][33];
+  wait_for_last();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
@@ -915,6 +929,21 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const uint4* dy, cons
 }
 
 // ---------------------------------------------------------------- host side
+
+// Launches a kernel that begins with wait_for_last.
+template <class... Params, class... Args>
+cudaError_t launch_next(void (*kernel)(Params...), int blocks, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // A view as the products see it: heads >= 1, rows as one batch element when they are
 // evenly spaced over all of them.
@@ -1051,14 +1080,13 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
   linear_kernel<kOrder><<<grid, kThreads, kSmem, stream>>>(ma, mb, a);
   e = cudaGetLastError();
   if (e == cudaSuccess && a.splits > 1) {
-    split_join_kernel<kOrder><<<int(rest) * (kBM * a.bn / 2048), 256, 0, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_next(split_join_kernel<kOrder>, int(rest) * (kBM * a.bn / 2048), 256, stream, a);
   }
   return e == cudaSuccess ? VSA_OK
                           : fail(VSA_ERR_CUDA, std::string("linear launch: ") + cudaGetErrorString(e));
 }
 
-vsa_status launch_few(const vsa_linear_args& q, cudaStream_t stream) {
+vsa_status launch_few(const vsa_plan_s* p, const vsa_linear_args& q, cudaStream_t stream) {
   FewArgs a = {};
   const View x = make_view(q.x, q.B, q.N, q.x_heads, q.C);
   a.x = x.ptr;
@@ -1077,7 +1105,13 @@ vsa_status launch_few(const vsa_linear_args& q, cudaStream_t stream) {
   a.bias = q.bias;
   a.bias_f32 = q.bias_type == VSA_F32;
   a.act = q.act;
-  linear_few_kernel<<<q.O / 8, kFewThreads, 0, stream>>>(a);
+  // Blocks that fit the SMs four apiece keep four pieces in flight (1,024 x 1,024: 2.7 against 3.4 us,
+  // 5,376 x 640: 7.2 against 7.8 us); more of them go five apiece with three (5,376 x 5,376: 12.0
+  // against 15.7 us, w from memory each time).
+  if (q.O / 8 <= 4 * sms(p))
+    linear_few_kernel<4, 4><<<q.O / 8, kFewThreads, 0, stream>>>(a);
+  else
+    linear_few_kernel<3, 5><<<q.O / 8, kFewThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VSA_OK
                           : fail(VSA_ERR_CUDA, std::string("linear launch: ") + cudaGetErrorString(e));
@@ -1095,7 +1129,7 @@ size_t linear_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
 }
 
 vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, void* ws, cudaStream_t stream) {
-  if (int64_t(q.B) * q.N <= kFewRows) return launch_few(q, stream);
+  if (int64_t(q.B) * q.N <= kFewRows) return launch_few(p, q, stream);
   View x = make_view(q.x, q.B, q.N, q.x_heads, q.C);
   if (rows_even(x)) flatten(&x);
   GemmArgs a = {};
@@ -1192,8 +1226,10 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     float* sums = static_cast<float*>(ws);
     colsum_kernel<<<dim3((q.O + 255) / 256, runs), 256, 0, stream>>>(
         out_view(q.dy, q.y_heads, q.O), make_div(q.N), int(M), q.O, colsum_rows(M), sums);
-    colsum_join_kernel<<<(q.O + 31) / 32, 1024, 0, stream>>>(sums, runs, q.O, q.db);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess)
+      e = launch_next(colsum_join_kernel, (q.O + 31) / 32, 1024, stream, static_cast<const float*>(sums), runs,
+                      int(q.O), q.db);
     if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
   }
   return VSA_OK;
