@@ -274,8 +274,9 @@ __device__ __forceinline__ int64_t col_offset(const OutView& v, int col) {
   return h * v.sh + (col - (h << v.shift));
 }
 
-// Programmatic launch: the kernel that joins partial sums is put on the GPU while the one that
-// writes them still runs (which says so at its start), and waits here for its end.
+// Programmatic launch: a call's later kernels are put on the GPU while the one before still runs
+// (every kernel lets them at its start), set themselves up, and wait for its end
+// before they touch memory.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -337,6 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();                      // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_last();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA
@@ -792,6 +794,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) linear_few_kernel(const _
 // would have done follows.  A thread takes eight columns of a row, a block 2,048 elements of a tile.
 template <int kOrder>
 __global__ void __launch_bounds__(256) split_join_kernel(const __grid_constant__ GemmArgs a) {
+  let_next_start();
   wait_for_last();
   const int octs = a.bn / 8, per_block = 256 / octs;       // rows of a block
   const int i = blockIdx.x / (kBM / per_block), part = blockIdx.x % (kBM / per_block);
@@ -860,6 +863,7 @@ __global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, const Div
                                                      int rows_per, float* part) {
   __shared__ float s[8][256];
   let_next_start();
+  wait_for_last();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 256 + 8 * lane;
   float2 acc[4] = {};
@@ -930,18 +934,20 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const uint4* dy, cons
 
 // ---------------------------------------------------------------- host side
 
-// Launches a kernel that begins with wait_for_last.
+// Launches a kernel; `after` another one of the same call it may start under that one's end.
 template <class... Params, class... Args>
-cudaError_t launch_next(void (*kernel)(Params...), int blocks, int threads, cudaStream_t stream, Args... args) {
+cudaError_t launch_on(cudaStream_t stream, bool after, void (*kernel)(Params...), dim3 blocks, int threads,
+                      size_t smem, const Args&... args) {
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.gridDim = blocks;
   cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = after ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1057,7 +1063,7 @@ int colsum_runs(int64_t M) { return int(std::max<int64_t>(1, (M + colsum_rows(M)
 
 template <int kOrder>
 vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv, int b_box,
-                  GemmArgs a, int64_t b_bytes, cudaStream_t stream) {
+                  GemmArgs a, int64_t b_bytes, bool after, cudaStream_t stream) {
   if (int64_t(a.m_tiles) * a.n_tiles >= (int64_t(1) << 31))
     return fail(VSA_ERR_UNSUPPORTED, "too many output tiles");
   CUtensorMap ma, mb;
@@ -1077,11 +1083,9 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
   a.status = p->d_status;
   const int64_t rest = int64_t(a.m_tiles) * a.n_tiles - a.whole, items = a.whole + rest * a.splits;
   const int grid = 2 * int(std::min<int64_t>(items, pairs_of(p)));
-  linear_kernel<kOrder><<<grid, kThreads, kSmem, stream>>>(ma, mb, a);
-  e = cudaGetLastError();
-  if (e == cudaSuccess && a.splits > 1) {
-    e = launch_next(split_join_kernel<kOrder>, int(rest) * (kBM * a.bn / 2048), 256, stream, a);
-  }
+  e = launch_on(stream, after, linear_kernel<kOrder>, dim3(unsigned(grid)), kThreads, kSmem, ma, mb, a);
+  if (e == cudaSuccess && a.splits > 1)
+    e = launch_on(stream, true, split_join_kernel<kOrder>, dim3(unsigned(rest * (kBM * a.bn / 2048))), 256, 0, a);
   return e == cudaSuccess ? VSA_OK
                           : fail(VSA_ERR_CUDA, std::string("linear launch: ") + cudaGetErrorString(e));
 }
@@ -1149,7 +1153,8 @@ vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, void* ws
   a.bias = q.bias;
   a.bias_f32 = q.bias_type == VSA_F32;
   a.act = q.act;
-  return launch<kForward>(p, x, 128, matrix(q.w, q.O, q.C), a.bn / 2, a, int64_t(q.O) * q.C * 2, stream);
+  return launch<kForward>(p, x, 128, matrix(q.w, q.O, q.C), a.bn / 2, a, int64_t(q.O) * q.C * 2, false,
+                          stream);
 }
 
 size_t linear_backward_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
@@ -1195,7 +1200,7 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.res = out_view(a.add ? q.dx_add : q.x_pre, q.x_heads, q.C);
     a.act = q.x_act;
     const vsa_status st = launch<kDgrad>(p, g, 128, matrix(q.w, q.O, q.C), kBK, a,
-                                         int64_t(q.O) * q.C * 2, stream);
+                                         int64_t(q.O) * q.C * 2, false, stream);
     if (st != VSA_OK) return st;
   }
   if (q.dw != nullptr) {
@@ -1218,18 +1223,19 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.y = OutView{static_cast<uint16_t*>(q.dw), 0, 0, q.C, 31};
     a.partial = static_cast<float*>(ws);
     // the rows are long: all column tiles of one group share the pass over them
-    const vsa_status st = launch<kWgrad>(p, g, kBK, x, kBK, a, 0, stream);
+    const vsa_status st = launch<kWgrad>(p, g, kBK, x, kBK, a, 0, q.dx.ptr != nullptr, stream);
     if (st != VSA_OK) return st;
   }
   if (q.db != nullptr) {
     const int runs = colsum_runs(M);
     float* sums = static_cast<float*>(ws);
-    colsum_kernel<<<dim3((q.O + 255) / 256, runs), 256, 0, stream>>>(
-        out_view(q.dy, q.y_heads, q.O), make_div(q.N), int(M), q.O, colsum_rows(M), sums);
-    cudaError_t e = cudaGetLastError();
+    const bool after = q.dx.ptr != nullptr || q.dw != nullptr;
+    cudaError_t e = launch_on(stream, after, colsum_kernel, dim3(unsigned((q.O + 255) / 256), unsigned(runs)), 256,
+                              0, out_view(q.dy, q.y_heads, q.O), make_div(q.N), int(M), int(q.O),
+                              colsum_rows(M), sums);
     if (e == cudaSuccess)
-      e = launch_next(colsum_join_kernel, (q.O + 31) / 32, 1024, stream, static_cast<const float*>(sums), runs,
-                      int(q.O), q.db);
+      e = launch_on(stream, true, colsum_join_kernel, dim3(unsigned((q.O + 31) / 32)), 1024, 0,
+                    static_cast<const float*>(sums), runs, int(q.O), q.db);
     if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
   }
   return VSA_OK;
