@@ -408,8 +408,9 @@ vsa_status vsa_check_bounded_wait(vsa_plan plan, int32_t* result, void* stream);
 
 /* Test hook for the attention kernels' failure path (the pages have no
  * counterpart).  Sets the bound of every mbarrier wait of the kernels that
- * vsa_sparse_attn, vsa_sparse_attn_combine, vsa_sparse_attn_ref and
- * vsa_sparse_attn_backward launch from then on, process-wide, in ns of wall
+ * vsa_sparse_attn, vsa_sparse_attn_combine, vsa_sparse_attn_ref,
+ * vsa_sparse_attn_backward and, of vsa_block.h, vsa_linear and
+ * vsa_linear_backward launch from then on, process-wide, in ns of wall
  * time; 0 (or anything above it) restores the 2 s default.  With a bound of
  * a few microseconds their waits run out: the kernel records
  * VSA_ERR_DEVICE_TIMEOUT in the plan's status word, drains its own TMA loads

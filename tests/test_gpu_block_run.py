@@ -233,3 +233,39 @@ def test_repeats_are_bitwise_equal():
     assert all(torch.equal(a, b) for a, b in zip(*runs))
     x, w = randn(1, 1, 40, 4096), randn(2, 256, 4096, scale=0.02)
     assert torch.equal(vsa.vsa_linear(c.plan, x, w), vsa.vsa_linear(c.plan, x, w))
+
+
+def test_linear_abort_path():
+    """The linear kernel's own failure path, without a fault: with the bound of its waits cut to 100 ns
+    they run out, the kernel records VSA_ERR_DEVICE_TIMEOUT, drains its copies and products, frees
+    its tensor memory and returns; with the bound restored the same context computes as before."""
+    import time
+    plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4))
+    x, w = randn(1, 1, 3000, 1024), randn(2, 1024, 1024, scale=0.03)
+    want = vsa.vsa_linear(plan, x, w)
+    vsa.vsa_sync_status(plan)
+    # a wait looks at the clock every sixteenth poll, and a poll may sleep for some time: sums of 4,096 K
+    # blocks keep the epilogue waiting for over a millisecond
+    long_x = torch.zeros(1, 3000, 1 << 18, dtype=torch.bfloat16, device="cuda")
+    long_w = torch.zeros(1024, 1 << 18, dtype=torch.bfloat16, device="cuda")
+    try:
+        vsa.vsa_debug_set_wait_limit(100)
+        timed_out = False
+        for _ in range(5):                 # a wait that happened to finish in time: try again
+            t0 = time.perf_counter()
+            vsa.vsa_linear(plan, long_x, long_w)
+            try:
+                vsa.vsa_sync_status(plan)
+            except vsa.VsaError as e:
+                assert e.status == 6, e                  # VSA_ERR_DEVICE_TIMEOUT
+                timed_out = True
+            # a pair whose halves stopped at different copies drains for up to 2 s
+            assert time.perf_counter() - t0 < 10.0
+            if timed_out:
+                break
+        assert timed_out, "the kernel never gave up under a 100 ns bound"
+    finally:
+        vsa.vsa_debug_set_wait_limit(0)
+    vsa.vsa_sync_status(plan)
+    assert torch.equal(vsa.vsa_linear(plan, x, w), want)
+    vsa.vsa_sync_status(plan)

@@ -73,6 +73,7 @@ __device__ __forceinline__ uint32_t operator/(uint32_t n, const Div& v) {
 
 struct GemmArgs {
   unsigned int* status;
+  unsigned long long wait_ns;      // bound of every wait
   int bn;                          // columns of a tile: 256 or 128
   int m_tiles, n_tiles, group;     // output tiles and the column group of the order
   Div by_group, by_width, by_last; // tiles of a group; its columns, and the last group's
@@ -111,11 +112,6 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
-}
-// wait_bar by a whole warp.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned int* status, unsigned int where) {
-  return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort_flag, status, where));
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -268,6 +264,12 @@ __device__ __forceinline__ uint4 pack(const float2* f) {
                     pack_bf16(f[3].x, f[3].y));
 }
 
+// wait_bar by a whole warp.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          const GemmArgs& a, unsigned int where) {
+  return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort_flag, a.status, where, a.wait_ns));
+}
+
 // Column col of a view (a block of 64 columns lies within a head), less its row.
 __device__ __forceinline__ int64_t col_offset(const OutView& v, int col) {
   const int h = col >> v.shift;
@@ -377,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ca[0] = (m - ha[0] * a.rows_b) * kBM + rank * 128;
         }
         for (int kb = k0; kb < k1; ++kb, ++g) {
-          if (g >= uint32_t(kStages) && !wait_warp(empty + 8 * s, phase, abort_flag, a.status, 31)) {
+          if (g >= uint32_t(kStages) && !wait_warp(empty + 8 * s, phase, abort_flag, a, 31)) {
             ok = false;
             break;
           }
@@ -437,14 +439,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Item it = item_of(t, a);
         const int nk = it.k1 - it.k0;
         const int buf = lt & 1;
-        if (lt >= 2 && !wait_warp(acc_empty + 8 * buf, ((lt >> 1) - 1) & 1, abort_flag, a.status, 32)) {
+        if (lt >= 2 && !wait_warp(acc_empty + 8 * buf, ((lt >> 1) - 1) & 1, abort_flag, a, 32)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t acc = tmem + buf * 256;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!wait_warp(full + 8 * s, phase, abort_flag, a.status, 33)) {
+          if (!wait_warp(full + 8 * s, phase, abort_flag, a, 33)) {
             ok = false;
             break;
           }
@@ -582,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) rr[i] = make_uint4(0u, 0u, 0u, 0u);
       load_res(0);
-      if (!wait_warp(acc_full + 8 * buf, (lt >> 1) & 1, abort_flag, a.status, 34)) break;
+      if (!wait_warp(acc_full + 8 * buf, (lt >> 1) & 1, abort_flag, a, 34)) break;
       tc_fence_after();
       uint32_t v[32];
       tmem_ld32(acc, v);
@@ -1063,7 +1065,7 @@ int colsum_runs(int64_t M) { return int(std::max<int64_t>(1, (M + colsum_rows(M)
 
 template <int kOrder>
 vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv, int b_box,
-                  GemmArgs a, int64_t b_bytes, bool after, cudaStream_t stream) {
+                  GemmArgs a, bool after, cudaStream_t stream) {
   if (int64_t(a.m_tiles) * a.n_tiles >= (int64_t(1) << 31))
     return fail(VSA_ERR_UNSUPPORTED, "too many output tiles");
   CUtensorMap ma, mb;
@@ -1072,8 +1074,12 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
   cudaError_t e = cudaFuncSetAttribute(linear_kernel<kOrder>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
-  const int64_t groups = std::max<int64_t>(1, (b_bytes + (int64_t(32) << 20) - 1) >> 25);
-  a.group = int(std::max<int64_t>(1, (a.n_tiles + groups - 1) / groups));
+  // Groups of at most 14 column tiles: the 74 tiles in work at a time are then some 5 x 14, and share
+  // their rows of A and columns of B in L2.  At 33,920 x 5,376 x 7,168 (28 or 21 column tiles) the weight
+  // gradient took 2,040 us with 14, 2,064 with 10 and 2,138 with all 28 (its DRAM reads fall from 8.5 to
+  // 4.5 GB, and with them the power that holds the clock down); the others stay within 2 %.
+  const int groups = (a.n_tiles + 13) / 14;
+  a.group = (a.n_tiles + groups - 1) / groups;
   a.by_group = make_div(int64_t(a.m_tiles) * a.group);
   a.by_width = make_div(a.group);
   a.by_last = make_div(a.n_tiles - (a.n_tiles - 1) / a.group * a.group);
@@ -1081,6 +1087,7 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
   a.by_rows_b = make_div(a.rows_b);
   a.by_nrow = make_div(a.Nrow);
   a.status = p->d_status;
+  a.wait_ns = wait_limit_ns();
   const int64_t rest = int64_t(a.m_tiles) * a.n_tiles - a.whole, items = a.whole + rest * a.splits;
   const int grid = 2 * int(std::min<int64_t>(items, pairs_of(p)));
   e = launch_on(stream, after, linear_kernel<kOrder>, dim3(unsigned(grid)), kThreads, kSmem, ma, mb, a);
@@ -1153,8 +1160,7 @@ vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, void* ws
   a.bias = q.bias;
   a.bias_f32 = q.bias_type == VSA_F32;
   a.act = q.act;
-  return launch<kForward>(p, x, 128, matrix(q.w, q.O, q.C), a.bn / 2, a, int64_t(q.O) * q.C * 2, false,
-                          stream);
+  return launch<kForward>(p, x, 128, matrix(q.w, q.O, q.C), a.bn / 2, a, false, stream);
 }
 
 size_t linear_backward_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
@@ -1199,8 +1205,7 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.add = q.dx_add.ptr != nullptr;
     a.res = out_view(a.add ? q.dx_add : q.x_pre, q.x_heads, q.C);
     a.act = q.x_act;
-    const vsa_status st = launch<kDgrad>(p, g, 128, matrix(q.w, q.O, q.C), kBK, a,
-                                         int64_t(q.O) * q.C * 2, false, stream);
+    const vsa_status st = launch<kDgrad>(p, g, 128, matrix(q.w, q.O, q.C), kBK, a, false, stream);
     if (st != VSA_OK) return st;
   }
   if (q.dw != nullptr) {
@@ -1222,8 +1227,7 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.Nrow = q.O;
     a.y = OutView{static_cast<uint16_t*>(q.dw), 0, 0, q.C, 31};
     a.partial = static_cast<float*>(ws);
-    // the rows are long: all column tiles of one group share the pass over them
-    const vsa_status st = launch<kWgrad>(p, g, kBK, x, kBK, a, 0, q.dx.ptr != nullptr, stream);
+    const vsa_status st = launch<kWgrad>(p, g, kBK, x, kBK, a, q.dx.ptr != nullptr, stream);
     if (st != VSA_OK) return st;
   }
   if (q.db != nullptr) {
