@@ -22,6 +22,16 @@
 //
 // Every wait is bounded (abort flag and status word); the pair meets at cluster
 // barriers before its first and after its last signal.
+//
+// Measured (B200): 33,920 x 5,376 -> 7,168 with bias, GELU and pre-activation out 1.75-2.0 ms = 1,300-1,490
+// TFLOP/s, the library's plain product of the same operands 1.65-1.9 ms in the same runs; gradients 1.75-2.1
+// ms each.  The tensor pipe is active 99 % of the time (ncu) at the 1.1-1.25 GHz to which the 1 kW cap takes the
+// clock: power bounds it.  2,048 x 5,376 x 5,376: 86 us forward, 77 us weight gradient (library 86-88 and 79).
+// 9,772 x 1,024 -> 1,024 from heads with bias and residual 26.8 us (three waves of 74 tiles for 2.1; library
+// without them 18.7).  On the way: one lane on the producer's and issuer's loops with divisions
+// in them 1,050-1,250 TFLOP/s, whole warps without divisions 1,400-1,500; branches for every eight values and
+// scalar arithmetic in the epilogue 45 us in place of 34 (4,096 x 1,024 -> 4,096, GELU); cluster-scope
+// releases, which wait for a warp's stores, another 2 us.
 #include <algorithm>
 
 #include "block_internal.h"

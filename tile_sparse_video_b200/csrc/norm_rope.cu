@@ -16,6 +16,13 @@
 // A lane's 8 channels are four pairs of the rotation: 8c .. 8c+7 where pairs are
 // neighbours, and 4c .. 4c+3 with P+4c .. P+4c+3 where they are halves (two 8-byte
 // accesses in place of one of 16 bytes, and no exchange between lanes).
+//
+// Measured (B200, device time, share of the measured 6,549 GB/s copy rate): Q, K and V of 104,704
+// tokens x 42 heads into tiles with their means 1,092 us (6.81 GB, 95 %); the rotation alone of 33,920 x 42 on
+// a [B,N,H,D] tensor 116 us (96 %); the backward of Q, K and V there 460 us (97 %); Q and K of 9,772
+// x 8 out of one [B,N,3,H,D] projection 19.7 us (80 MB, 62 %: start and end of so short a kernel);
+// two heads of 366 tokens 4 us (launch).  A warp per tile and head with its loads in registers, which
+// looked the angles up for every row and head, took 2,031, 252, 815, 39 and 8 us.
 #include <algorithm>
 
 #include "block_internal.h"
@@ -188,13 +195,15 @@ struct Block {
   static constexpr int kRows = kPass * kU;
   static constexpr uint32_t kStage = kThreads * kU * 16;   // slots of one tensor's rows
 };
+// Heads in flight.  With two the tiles take 1,125 us in place of 1,101; with four only one block of
+// the backward fits an SM (550 us in place of 460).
 constexpr int kStages = 3;
 // Heads of a tile item, at most: its column sums (4 KB a head of 128 channels, 64 KB) and the slots
 // (48 KB) leave room for two blocks on an SM.
 constexpr int kMaxGroup = 16;
 
 template <int kD, bool kHalves, bool kTiled, int kThreads, int kU>
-__global__ void __launch_bounds__(kThreads, kTiled ? 2 : 4)
+__global__ void __launch_bounds__(kThreads, kTiled ? 2 : 6)
     norm_rope_kernel(const __grid_constant__ FwdArgs a) {
   using Bl = Block<kD, kThreads, kU>;
   constexpr int kCpr = Bl::kCpr;
@@ -455,8 +464,10 @@ RopeArgs rope_args(const vsa_rope_s* r, int inverse) {
   return a;
 }
 
-// Heads of an item.  An item costs its heads and a start of about two more; the blocks
-// come in waves of `slots`: the group that makes the waves shortest.
+// Heads of an item.  An item costs its heads and a start of about two more (its rows' indices and
+// angles, and the first heads' way from memory); the blocks come in waves of `slots`: the
+// group that makes the waves shortest.  (One head an item: small layer 41 us, eight: 27 us; all 42 heads
+// an item or a sixteenth of the waves: 1,186 and 1,318 us at 104,704 tokens.)
 template <class Args>
 bool set_items(Args* a, const vsa_plan_s* p, int64_t row_blocks, int B, int H, int n, int64_t slots,
                int max_group, int64_t* items) {
@@ -500,11 +511,12 @@ vsa_status launch_norm_rope(const vsa_plan_s* p, const vsa_rope_s* rope, const H
   a.eps = eps;
   a.block_len = p->d_block_len;
   a.N = p->n_tokens;
-  // rows of an item: a tile, or 32 (64 of 64 channels) in natural order
-  const int64_t row_blocks = tiled ? p->n_tiles : (p->n_tokens + 4096 / D - 1) / (4096 / D);
+  // rows of an item: a tile, or 16 (32 of 64 channels) in natural order, where a row a lane leaves room
+  // for six blocks an SM (two rows and four blocks: 123 us in place of 116 at 33,920 x 42)
+  const int64_t row_blocks = tiled ? p->n_tiles : (p->n_tokens + 2048 / D - 1) / (2048 / D);
   a.R = p->R;
   int64_t items = 0;
-  if (!set_items(&a, p, row_blocks, B, H, n, int64_t(sms(p)) * (tiled ? 2 : 4),
+  if (!set_items(&a, p, row_blocks, B, H, n, int64_t(sms(p)) * (tiled ? 2 : 6),
                  tiled ? kMaxGroup : H, &items))
     return fail(VSA_ERR_UNSUPPORTED, "too many heads and rows for one launch");
   const bool halves = rope != nullptr && rope->halves;
@@ -519,12 +531,12 @@ vsa_status launch_norm_rope(const vsa_plan_s* p, const vsa_rope_s* rope, const H
     if (tiled)
       VSA_LAUNCH(128, true, 4)
     else
-      VSA_LAUNCH(128, false, 2)
+      VSA_LAUNCH(128, false, 1)
   } else {
     if (tiled)
       VSA_LAUNCH(64, true, 2)
     else
-      VSA_LAUNCH(64, false, 2)
+      VSA_LAUNCH(64, false, 1)
   }
 #undef VSA_LAUNCH
   return e == cudaSuccess ? VSA_OK
@@ -571,7 +583,7 @@ vsa_status launch_norm_rope_backward(const vsa_plan_s* p, const vsa_rope_s* rope
     if (tiled)
       VSA_LAUNCH(64, true, 2);
     else
-      VSA_LAUNCH(64, false, 2);
+      VSA_LAUNCH(64, false, 1);
   }
 #undef VSA_LAUNCH
   if (e == cudaSuccess && gains) {
