@@ -201,6 +201,7 @@ constexpr int kStages = 3;
 // Heads of a tile item, at most: its column sums (4 KB a head of 128 channels, 64 KB) and the slots
 // (48 KB) leave room for two blocks on an SM.
 constexpr int kMaxGroup = 16;
+constexpr int kGradRows = 64;         // rows of an item of the backward
 
 template <int kD, bool kHalves, bool kTiled, int kThreads, int kU>
 __global__ void __launch_bounds__(kThreads, kTiled ? 2 : 6)
@@ -523,6 +524,7 @@ vsa_status launch_norm_rope(const vsa_plan_s* p, const vsa_rope_s* rope, const H
   cudaError_t e;
 #define VSA_LAUNCH(DD, TL, U)                                                                     \
   {                                                                                               \
+    static_assert(Block<DD, 256, U>::kRows == (TL ? 64 : 2048 / DD), "rows of a pass or an item"); \
     const uint32_t smem = kStages * Block<DD, 256, U>::kStage + (TL ? a.group * 8 * DD * 4 : 0);  \
     e = halves ? launch(norm_rope_kernel<DD, true, TL, 256, U>, items, n, 256, smem, a, stream)   \
                : launch(norm_rope_kernel<DD, false, TL, 256, U>, items, n, 256, smem, a, stream); \
@@ -563,27 +565,31 @@ vsa_status launch_norm_rope_backward(const vsa_plan_s* p, const vsa_rope_s* rope
   a.partial = static_cast<float*>(ws);
   a.rows = tiled ? p->n_padded : p->n_tokens;
   int64_t items = 0;
-  if (!set_items(&a, p, (a.rows + 63) / 64, B, H, n, max_blocks(p), H, &items))
+  if (!set_items(&a, p, (a.rows + kGradRows - 1) / kGradRows, B, H, n, max_blocks(p), H, &items))
     return fail(VSA_ERR_UNSUPPORTED, "too many heads and rows for one launch");
   a.n_items = unsigned(items);
   const int64_t blocks = std::min<int64_t>(items, max_blocks(p));
   const bool halves = rope != nullptr && rope->halves;
   cudaError_t e;
-#define VSA_LAUNCH(DD, TL, U)                                                                  \
-  e = halves ? launch(norm_rope_backward_kernel<DD, true, TL, 256, U>, blocks, n, 256,         \
-                      2 * kStages * Block<DD, 256, U>::kStage, a, stream)                      \
-             : launch(norm_rope_backward_kernel<DD, false, TL, 256, U>, blocks, n, 256,        \
-                      2 * kStages * Block<DD, 256, U>::kStage, a, stream)
+#define VSA_LAUNCH(DD, TL, U)                                                                 \
+  {                                                                                           \
+    static_assert(Block<DD, 256, U>::kRows == kGradRows, "rows of an item");                  \
+    const uint32_t smem = 2 * kStages * Block<DD, 256, U>::kStage;                            \
+    e = halves ? launch(norm_rope_backward_kernel<DD, true, TL, 256, U>, blocks, n, 256,      \
+                        smem, a, stream)                                                      \
+               : launch(norm_rope_backward_kernel<DD, false, TL, 256, U>, blocks, n, 256,     \
+                        smem, a, stream);                                                     \
+  }
   if (D == 128) {
     if (tiled)
-      VSA_LAUNCH(128, true, 4);
+      VSA_LAUNCH(128, true, 4)
     else
-      VSA_LAUNCH(128, false, 4);
+      VSA_LAUNCH(128, false, 4)
   } else {
     if (tiled)
-      VSA_LAUNCH(64, true, 2);
+      VSA_LAUNCH(64, true, 2)
     else
-      VSA_LAUNCH(64, false, 1);
+      VSA_LAUNCH(64, false, 2)
   }
 #undef VSA_LAUNCH
   if (e == cudaSuccess && gains) {
