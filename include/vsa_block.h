@@ -100,7 +100,8 @@ typedef struct vsa_head_tensor {
 } vsa_head_tensor;
 
 /* One launch for n tensors (1 .. VSA_MAX_HEAD_TENSORS), natural order in and out.
- * y may be x itself.  rope may be NULL when no tensor rotates. */
+ * y may be x itself; an output must not overlap anything else of the call.  rope may
+ * be NULL when no tensor rotates (and is not looked at then). */
 vsa_status vsa_norm_rope(vsa_plan plan, vsa_rope rope, const vsa_head_tensor* tensors, int n,
                          float eps, int B, int H, int D, void* stream);
 
@@ -195,7 +196,8 @@ vsa_status vsa_linear_backward(vsa_plan plan, const vsa_linear_grad_args* args, 
                                size_t ws_bytes, void* stream);
 
 /* out = dy * act'(pre), n bf16 elements each (n a multiple of 8), contiguous; out may
- * be dy or pre itself. */
+ * be dy or pre itself.  What is left of an activation's backward where its output does
+ * not go into vsa_linear (there x_pre does it in the product's epilogue). */
 vsa_status vsa_act_backward(vsa_plan plan, const void* dy, const void* pre, int act, void* out,
                             int64_t n, void* stream);
 

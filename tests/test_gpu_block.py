@@ -193,6 +193,22 @@ def test_norm_rope_broadcast_and_status():
     assert e.value.status == 1
 
 
+def test_rope_that_nothing_asks_for():
+    """Without a rotating tensor the rope is not looked at: one that is too wide for D, in halves, or of
+    another plan changes nothing."""
+    plan, other = vsa.Plan((9,), (2, 4, 4), (4, 4, 4)), vsa.Plan((3,), (1, 4, 4), (4, 4, 4))
+    x = randn(1, 1, 2, plan.n_tokens, 64)
+    item = [vsa.HeadTensor(x, rotate=False)]
+    want, = vsa.vsa_norm_rope(plan, item)
+    (want_t, _), = vsa.vsa_norm_rope_permute_pool(plan, item)
+    (want_g, _), = vsa.vsa_norm_rope_backward(plan, [vsa.HeadGrad(x, x, rotate=False)])
+    for rope in (vsa.Rope(plan, (44, 42, 42), halves=True), vsa.Rope(other, (24, 20, 20), halves=True)):
+        assert torch.equal(vsa.vsa_norm_rope(plan, item, rope)[0], want)
+        assert torch.equal(vsa.vsa_norm_rope_permute_pool(plan, item, rope)[0][0], want_t)
+        assert torch.equal(vsa.vsa_norm_rope_backward(plan, [vsa.HeadGrad(x, x, rotate=False)], rope)[0][0], want_g)
+    vsa.vsa_sync_status(plan)
+
+
 def test_norm_rope_refusals():
     plan = vsa.Plan((9,), (2, 4, 4), (4, 4, 4))
     other = vsa.Plan((8,), (2, 4, 4), (4, 4, 4))
@@ -448,3 +464,59 @@ def test_permute_pool_without_means():
     assert none is None and torch.equal(g_t, vsa.vsa_permute(plan, g))
     assert torch.equal(qbar, vsa.vsa_norm_rope_permute_pool(plan, [vsa.HeadTensor(q, rotate=False)])[0][1])
     vsa.vsa_sync_status(plan)
+
+
+def test_offsets_past_32_bits_norm_rope():
+    """2.25 G elements a tensor, token strides of 21,504: sampled rows at both ends."""
+    plan = vsa.Plan((256,), (32, 48, 68), (4, 8, 4))
+    rope = vsa.Rope(plan, (44, 42, 42))
+    N, H, D = plan.n_tokens, 168, 128
+    x = torch.empty(1, N, H, D, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for i in range(0, N, 16384):
+        x[:, i:i + 16384] = torch.randn(1, min(16384, N - i), H, D, generator=g, device="cuda")
+    assert x.numel() > 2 ** 31
+    x = x.transpose(1, 2)
+    tok = np.r_[0:3, 255:258, N // 2, N - 3:N]
+    ang = BO.angles(BO.positions((256,), (32, 48, 68)), (44, 42, 42))[tok]
+    heads = [0, 85, 167]
+    at = lambda t: t[:, heads][:, :, tok]
+    z = BO.head_norm(at(x), None, EPS)
+    want = BO.rotate(z, ang, False)
+    slack = rot_slack(z) + (D / 2 + 8) * 2.0 ** -24 * np.abs(z).max(-1, keepdims=True)
+    y, = vsa.vsa_norm_rope(plan, [vsa.HeadTensor(x)], rope, EPS)
+    close(at(y), want, slack, "natural")
+    del y
+    (y_t, _), = vsa.vsa_norm_rope_permute_pool(plan, [vsa.HeadTensor(x)], rope, EPS)
+    rows = plan.tables()["untile"][tok]
+    close(y_t[:, heads][:, :, rows], want, slack, "tiles")
+    # back through it: the gradient of the tiles is the tiles themselves
+    (dx, _), = vsa.vsa_norm_rope_backward(plan, [vsa.HeadGrad(y_t, x)], rope, EPS, tiled=True)
+    gr = BO.rotate(y_t[:, heads][:, :, rows], ang, False, inverse=True)
+    want, _ = BO.head_norm_backward(gr, at(x), None, EPS)
+    r = 1 / np.sqrt((f64(at(x)) ** 2).mean(-1, keepdims=True) + EPS)
+    big = np.abs(gr).max(-1, keepdims=True)
+    u = np.abs(f64(at(x)) * r).max(-1, keepdims=True)
+    close(at(dx), want, (2 * D + 32) * 2.0 ** -24 * r * (big + u * u * big), "dx")
+    vsa.vsa_sync_status(plan)
+
+
+def test_offsets_past_32_bits_linear():
+    """An output, and a gradient of it, of 2.37 G elements: sampled rows and columns at both ends."""
+    plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4))
+    M, C, Ow = 330001, 64, 7168
+    x, w, b = randn(1, 1, M, C), randn(2, Ow, C, scale=0.1), randn(3, Ow)
+    y = vsa.vsa_linear(plan, x, w, b)
+    assert y.numel() > 2 ** 31
+    rows = np.r_[0:3, M // 2, M - 3:M]
+    p = BO.linear(x[:, rows], w, b)
+    close(y[:, rows], p, dot_slack(f64(x[:, rows]), f64(w)) + 2.0 ** -23 * np.abs(p), "y")
+    dx, dw, db = vsa.vsa_linear_backward(plan, y, x, w)
+    vsa.vsa_sync_status(plan)
+    gr = f64(y[:, rows])
+    close(dx[:, rows], gr @ f64(w), dot_slack(gr, f64(w).T), "dx")
+    cols = [0, 3584, Ow - 1]
+    gc, xr = f64(y[0][:, cols]), f64(x[0])
+    close(dw[cols], gc.T @ xr, dot_slack(gc.T, xr.T), "dw")
+    # fp32 sums in a chain of 88 rows, 8 warps, 15 runs and 32 rows of runs
+    close(db[cols], gc.sum(0), 160 * 2.0 ** -24 * np.abs(gc).sum(0), "db", half_step=0.0)

@@ -335,6 +335,7 @@ static vsa_status norm_rope_forward(vsa_plan p, vsa_rope rope, const vsa_head_te
     return fail(VSA_ERR_INVALID_ARG, "n must be in [1, 4] and tensors not NULL");
   VSA_TRY(check_eps(eps));
   const bool empty = int64_t(B) * H == 0 || p->n_tokens == 0;
+  bool turns = false;
   HeadTensorArgs t[VSA_MAX_HEAD_TENSORS] = {};
   for (int i = 0; i < n; ++i) {
     const vsa_head_tensor& s = tensors[i];
@@ -343,6 +344,7 @@ static vsa_status norm_rope_forward(vsa_plan p, vsa_rope rope, const vsa_head_te
     if (s.gain != nullptr && !s.norm)
       return fail(VSA_ERR_INVALID_ARG, "a gain needs norm = 1");
     if (s.rotate) VSA_TRY(check_rope(p, rope, D));
+    turns = turns || s.rotate;
     if (empty) continue;
     VSA_TRY(check_view(s.x, B, H, p->n_tokens, D, false, 0, "x"));
     if (tiled) {
@@ -364,7 +366,9 @@ static vsa_status norm_rope_forward(vsa_plan p, vsa_rope rope, const vsa_head_te
     t[i].pooled = s.pooled;
   }
   if (empty) return VSA_OK;
-  return launch_norm_rope(p, rope, t, n, eps, 0, tiled, B, H, D, static_cast<cudaStream_t>(stream));
+  // a rope that no tensor asked for was not looked at, and is not used
+  return launch_norm_rope(p, turns ? rope : nullptr, t, n, eps, 0, tiled, B, H, D,
+                          static_cast<cudaStream_t>(stream));
 }
 
 vsa_status vsa_norm_rope(vsa_plan p, vsa_rope rope, const vsa_head_tensor* tensors, int n, float eps,
@@ -398,7 +402,7 @@ vsa_status vsa_norm_rope_backward(vsa_plan p, vsa_rope rope, const vsa_head_grad
   VSA_TRY(check_eps(eps));
   const bool empty = int64_t(B) * H == 0 || p->n_tokens == 0;
   const int64_t N = p->n_tokens;
-  bool gains = false;
+  bool gains = false, turns = false;
   HeadGradArgs t[VSA_MAX_HEAD_TENSORS] = {};
   for (int i = 0; i < n; ++i) {
     const vsa_head_grad& s = grads[i];
@@ -409,6 +413,7 @@ vsa_status vsa_norm_rope_backward(vsa_plan p, vsa_rope rope, const vsa_head_grad
     if (s.d_gain != nullptr) VSA_TRY(check_ptr(s.d_gain, "d_gain"));
     if (s.rotate) VSA_TRY(check_rope(p, rope, D));
     gains = gains || s.d_gain != nullptr;
+    turns = turns || s.rotate;
     if (empty) continue;
     if (s.norm) VSA_TRY(check_view(s.x, B, H, N, D, false, 0, "x"));
     VSA_TRY(check_view(s.dx, B, H, N, D, true, 8, "dx"));
@@ -446,7 +451,7 @@ vsa_status vsa_norm_rope_backward(vsa_plan p, vsa_rope rope, const vsa_head_grad
                   "workspace missing or too small (see vsa_norm_rope_backward_workspace_size)");
     VSA_TRY(check_ptr(ws, "ws"));
   }
-  return launch_norm_rope_backward(p, rope, t, n, eps, tiled == 1, B, H, D, ws, st);
+  return launch_norm_rope_backward(p, turns ? rope : nullptr, t, n, eps, tiled == 1, B, H, D, ws, st);
 }
 
 vsa_status vsa_linear_workspace_size(vsa_plan p, int B, int64_t N, int C, int O, size_t* bytes) {
