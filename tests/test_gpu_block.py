@@ -353,6 +353,34 @@ def test_linear_backward_through_activation(c, act):
     close(dx, BO.heads(wx * slope, xh), BO.heads(slack, xh), "dx")
 
 
+@pytest.mark.parametrize("c", [(1, 5000, 0, 520, 0, 1000), (2, 2600, 4, 512, 8, 1024), (1, 2500, 0, 512, 0, 2184)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_linear_full_waves_and_strips(c):
+    """More tiles than pairs of SMs: the last ones are cut into strips of 64 columns, some of them
+    over the last column; what lies beside the result stays as it was."""
+    B, N, xh, C, yh, Ow = c
+    plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4))
+    x, w, bias = rows_or_heads(1, B, N, xh, C), randn(2, Ow, C, scale=C ** -0.5), randn(3, Ow)
+    res = rows_or_heads(4, B, N, yh, Ow)
+    wide = torch.full((B, yh, N, Ow // yh + 64) if yh else (B, N, Ow + 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    width = Ow // yh if yh else Ow
+    y, pre = wide[..., :width], torch.empty_like(res)
+    vsa.vsa_linear(plan, x, w, bias, act="gelu_tanh", residual=res, pre=pre, y=y)
+    vsa.vsa_sync_status(plan)
+    assert bool((wide[..., width:] == 7.0).all())
+    p = BO.linear(x, w, bias)
+    slack = dot_slack(BO.rows(x), f64(w)) + 2.0 ** -23 * np.abs(p)
+    close(pre, BO.heads(p, yh), BO.heads(slack, yh), "pre")
+    want = BO.act("gelu_tanh", p) + BO.rows(res)
+    close(y, BO.heads(want, yh), BO.heads(act_slack("gelu_tanh", p, slack) + 2.0 ** -24 * np.abs(want), yh), "y")
+
+
+@pytest.mark.parametrize("c", [(1, 2500, 0, 2184, 0, 512), (1, 520, 0, 2184, 0, 2504)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_linear_backward_full_waves_and_strips(c):
+    test_linear_backward(c)
+
+
 @pytest.mark.parametrize("act", ["identity", "sigmoid", "gelu_tanh", "silu"])
 def test_act_backward(act):
     plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4))

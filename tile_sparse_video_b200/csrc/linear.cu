@@ -27,8 +27,7 @@
 // TFLOP/s, the library's plain product of the same operands 1.65-1.9 ms in the same runs; gradients 1.75-2.1
 // ms each.  The tensor pipe is active 99 % of the time (ncu) at the 1.1-1.25 GHz to which the 1 kW cap takes the
 // clock: power bounds it.  2,048 x 5,376 x 5,376: 86 us forward, 77 us weight gradient (library 86-88 and 79).
-// 9,772 x 1,024 -> 1,024 from heads with bias and residual 26.8 us (three waves of 74 tiles for 2.1; library
-// without them 18.7).  On the way: one lane on the producer's and issuer's loops with divisions
+// 9,772 x 1,024 -> 1,024 18.8 us (library 18.7), with bias and residual 21.7.  On the way: one lane on the producer's and issuer's loops with divisions
 // in them 1,050-1,250 TFLOP/s, whole warps without divisions 1,400-1,500; branches for every eight values and
 // scalar arithmetic in the epilogue 45 us in place of 34 (4,096 x 1,024 -> 4,096, GELU); cluster-scope
 // releases, which wait for a warp's stores, another 2 us.
@@ -87,9 +86,10 @@ struct GemmArgs {
   int bn;                          // columns of a tile: 256 or 128
   int m_tiles, n_tiles, group;     // output tiles and the column group of the order
   Div by_group, by_width, by_last; // tiles of a group; its columns, and the last group's
-  Div by_splits, by_rows_b, by_nrow;
-  // whole tiles come first, in full waves; the rest are split along K, k_split blocks each
-  int k_blocks, k_split, splits, whole;
+  Div by_parts, by_rows_b, by_nrow; // by_parts: splits or strips of a tile
+  // whole tiles come first, in full waves; the rest are split along K, k_split blocks each, or
+  // cut into strips of columns
+  int k_blocks, k_split, splits, strips, whole;
   int rows_b;                      // row blocks (tiles, or K blocks in wgrad) per batch element
   int64_t N;                       // rows of a batch element of the TMA views
   int64_t M;                       // valid rows of the output (rows of dw in wgrad)
@@ -170,14 +170,18 @@ __device__ __forceinline__ void decode(uint32_t tile, const GemmArgs& a, int& m,
   m = int(last ? r / a.by_last : r / a.by_width);
   n = first + int(r) - m * int(last ? a.by_last.d : a.by_width.d);
 }
-// Work item t: a whole tile, or split sp of one.
+// Work item t: `width` columns from column `col` of a tile; sp >= 0 is a split of its K.
 struct Item {
-  int tile, sp, k0, k1;
+  int tile, sp, k0, k1, col, width;
 };
 __device__ __forceinline__ Item item_of(int t, const GemmArgs& a) {
-  if (t < a.whole) return {t, -1, 0, a.k_blocks};
-  const int u = t - a.whole, i = int(uint32_t(u) / a.by_splits), sp = u - i * a.splits;
-  return {a.whole + i, sp, sp * a.k_split, min(a.k_blocks, (sp + 1) * a.k_split)};
+  if (t < a.whole) return {t, -1, 0, a.k_blocks, 0, a.bn};
+  const int u = t - a.whole, i = int(uint32_t(u) / a.by_parts), part = u - i * int(a.by_parts.d);
+  if (a.strips > 1) {
+    const int width = a.bn / a.strips;
+    return {a.whole + i, -1, 0, a.k_blocks, part * width, width};
+  }
+  return {a.whole + i, a.splits > 1 ? part : -1, part * a.k_split, min(a.k_blocks, (part + 1) * a.k_split), 0, a.bn};
 }
 
 // Two fp32 values at a time: the epilogue's arithmetic is bound by its instructions.
@@ -301,7 +305,7 @@ __device__ __forceinline__ uint4* chunk_at(uint8_t* staging, int r, int q) {
 template <int kOrder>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                  const __grid_constant__ GemmArgs a) {
+                  const __grid_constant__ CUtensorMap tm_strip, const __grid_constant__ GemmArgs a) {
   constexpr bool kAMn = kOrder == kWgrad, kBMn = kOrder != kForward;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -318,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0);
   const int rank = int(cluster_rank());
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int items = a.whole + (a.m_tiles * a.n_tiles - a.whole) * a.splits;
+  const int items = a.whole + (a.m_tiles * a.n_tiles - a.whole) * int(a.by_parts.d);
 
   let_next_start();
   if (threadIdx.x == 0) {
@@ -362,13 +366,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // block of products takes 512 cycles, and a division by a variable some hundred.
       uint32_t g = 0, s = 0, phase = 1;  // K block, its stage, parity of the stage's last use
       bool ok = true;
-      const int half = a.bn / 2;         // this CTA's columns of the B block
       const uint32_t lead = at_leader(full);
       for (int t = pair; t < items && ok; t += pairs) {
         const Item it = item_of(t, a);
         int m, n;
         decode(it.tile, a, m, n);
-        const int b0 = n * a.bn + rank * half;
+        const int half = it.width / 2;   // this CTA's columns of the B block
+        const int b0 = n * a.bn + it.col + rank * half;
+        const CUtensorMap* map_b = kOrder == kForward && it.width < a.bn ? &tm_strip : &tm_b;
         const int k0 = it.k0, k1 = it.k1;
         // along K: block `i` of `per` in head (or batch element) `o`
         const int per = kAMn ? a.rows_b : a.ac.blocks;
@@ -400,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tma_load_4d(sa, &tm_a, bar, i * kBK, ca[0], o, ha[0]);
               const int k = o * a.ac.D + i * kBK;
               if (!kBMn) {
-                tma_load_4d(sb, &tm_b, bar, k, b0, 0, 0);
+                tma_load_4d(sb, map_b, bar, k, b0, 0, 0);
               } else {
                 tma_load_4d(sb, &tm_b, bar, b0, k, 0, 0);
                 if (half > 64) tma_load_4d(sb + kMnAtom, &tm_b, bar, b0 + 64, k, 0, 0);
@@ -441,13 +446,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA, for the pair
     if (rank == 0) {
-      const uint32_t idesc = idesc_bf16(kBM, a.bn, kAMn, kBMn);
       uint32_t s = 0, phase = 0;
       int lt = 0;
       bool ok = true;
       for (int t = pair; t < items && ok; t += pairs, ++lt) {
         const Item it = item_of(t, a);
         const int nk = it.k1 - it.k0;
+        const uint32_t idesc = idesc_bf16(kBM, it.width, kAMn, kBMn);
         const int buf = lt & 1;
         if (lt >= 2 && !wait_warp(acc_empty + 8 * buf, ((lt >> 1) - 1) & 1, abort_flag, a, 32)) {
           ok = false;
@@ -494,17 +499,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- epilogue
     const int quad = warp & 3;                       // TMEM lane quadrant of this warp
     const int side = (warp - 2) >> 2;                // first or second half of the columns
-    const int half = a.bn / 2;
     uint8_t* st = staging + (warp - 2) * (32 * 64);
     float* bias = s_bias + (warp - 2) * 128;
     const int row0 = rank * 128 + quad * 32;         // first row of the warp in the tile
     float next_bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // column 32 i + lane of the next tile
     const auto read_bias = [&](int t) {
       int m, n;
-      decode(item_of(t, a).tile, a, m, n);
+      const Item it = item_of(t, a);
+      const int half = it.width / 2;
+      decode(it.tile, a, m, n);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int col = n * a.bn + side * half + 32 * i + lane;
+        const int col = n * a.bn + it.col + side * half + 32 * i + lane;
         next_bias[i] = 0.0f;
         if (32 * i < half && col < a.cols)
           next_bias[i] =
@@ -518,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Item it = item_of(t, a);
       int m, n;
       decode(it.tile, a, m, n);
-      const int buf = lt & 1;
+      const int buf = lt & 1, half = it.width / 2;
       const uint32_t acc = tmem + buf * 256 + (uint32_t(quad * 32) << 16) + uint32_t(side * half);
       // four lanes write a row's 64 bytes: this lane's rows are 8 i + lane / 4
       uint32_t tok[4], bat[4];
@@ -540,7 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       const int q = lane & 3;                        // and its chunk of them
-      const int col_w = n * a.bn + side * half;      // first column of the warp
+      const int col_w = n * a.bn + it.col + side * half;      // first column of the warp
       const bool with_bias = kOrder == kForward && a.bias != nullptr;
       if (with_bias) {
         // the tile's biases were read during the tile before
@@ -1020,47 +1026,67 @@ int sms(const vsa_plan_s* p) { return p->num_sms > 0 ? p->num_sms : 148; }
 
 int pairs_of(const vsa_plan_s* p) { return std::max(1, sms(p) / 2); }
 
-// Columns of a tile (256 or 128), and into how many splits of K the tiles go that are over after
-// the full waves, by the time it should take, in us: a wave of tiles over the pairs of SMs takes
-// 0.35 a K block with 256 columns and 0.25 with 128 (measured: 29 and 20 us at K = 5,376; a
-// tile of 128 columns wants half as much again of operand bytes a product) and one for its
-// turn; splits cost the join, a launch and two passes over their fp32 partial sums at some 4 TB/s.
+// Columns of a tile (256 or 128), and what becomes of the tiles that are over after the full waves:
+// whole, split along K, or cut into strips of columns (64 or 128 wide; the gradients' boxes of 64
+// columns a CTA leave them 128), by the time it should take, in us.  A wave of tiles over the pairs
+// of SMs takes 0.35 a K block with 256 columns, 0.25 with 128 and 0.22 with 64 (measured: 29 and
+// 20 us at K = 5,376 for the first two; narrow tiles want more operand bytes a product), and one
+// for its turn; its epilogue takes 14 ns a column and runs under the next wave's products.  Splits
+// of K cost the join: a launch under the products' end and two passes over their fp32 partial sums, at
+// some 4 TB/s.
+// Strips cost their operands' bytes, and shorten the last epilogue along with the last products.
+// Measured with whole tiles, the best strips and the best split: 9,772 x 1,024 -> 1,024 with residual
+// 24.4, 21.6, 27.6 us; 3,000 x 512 -> 2,048 11.7, 10.6, 17.1; 9,772 x 4,096 -> 1,024 71.5, 68.6, 68.1;
+// 1,024 x 5,376 -> 5,376 56.5, 50.8, 49.4; 256 rows of it 22.7 (128 columns), 22.9, 21.0.
 struct Tiling {
-  int bn, splits, k_split;
+  int bn, splits, k_split, strips;
   int64_t whole, split_tiles;
   size_t bytes() const {
     return splits > 1 ? size_t(splits) * size_t(split_tiles) * kBM * size_t(bn) * sizeof(float) : 0;
   }
 };
-Tiling tiling(const vsa_plan_s* p, int64_t m_tiles, int64_t M, int cols, int k_blocks, bool may_split) {
-  Tiling best = {256, 1, k_blocks, 0, 0};
+Tiling tiling(const vsa_plan_s* p, int64_t m_tiles, int64_t M, int cols, int k_blocks, bool may_split, bool narrow) {
+  const auto products = [](int width, int blocks) {
+    return blocks * (width == 256 ? 0.35 : width == 128 ? 0.25 : 0.22) + 1;
+  };
+  const auto epilogue = [](int width) { return 0.014 * width; };
+  Tiling best = {256, 1, k_blocks, 1, 0, 0};
   double least = 1e300;
   for (const int bn : {256, 128}) {
     const int64_t tiles = m_tiles * ((cols + bn - 1) / bn), rest = tiles % pairs_of(p);
-    const double block = bn == 256 ? 0.35 : 0.25;
-    const int most = may_split && rest > 0
-                         ? int(std::min<int64_t>({16, k_blocks / 4, pairs_of(p) / rest}))
-                         : 1;
-    for (int want = 1; want <= std::max(1, most); ++want) {
-      const int k_split = (k_blocks + want - 1) / want, s = (k_blocks + k_split - 1) / k_split;
-      const double join = s > 1 ? 3.0 + double(s) * double(rest) * double(std::min<int64_t>(M, kBM)) * bn * 8 / 4e6 : 0.0;
-      const double t = double(tiles / pairs_of(p)) * (k_blocks * block + 1) +
-                       (rest > 0 ? k_split * block + 1 : 0) + join;
+    const double waves = double(tiles / pairs_of(p)), P = products(bn, k_blocks), E = epilogue(bn);
+    // when the epilogues of the full waves end, and when a product after them may start (its
+    // accumulator is that of the wave before the last)
+    const double done = waves > 0 ? waves * std::max(P, E) + std::min(P, E) : 0;
+    const double idle = std::max(waves * P, done - std::max(P, E));
+    const auto consider = [&](int splits, int k_split, int strips) {
+      const int width = bn / strips;
+      const double join = splits > 1 ? 1.0 + double(splits) * double(rest) * double(std::min<int64_t>(M, kBM)) * bn * 8 / 4e6 : 0.0;
+      const double t = rest > 0 ? std::max(done, idle + products(width, k_split)) + epilogue(width) + join : done;
       if (t < least) {
         least = t;
-        best = {bn, s, k_split, s > 1 ? tiles - rest : tiles, s > 1 ? rest : 0};
+        best = {bn, splits, k_split, strips, splits * strips > 1 ? tiles - rest : tiles, splits > 1 ? rest : 0};
       }
+    };
+    const int64_t parts = rest > 0 ? pairs_of(p) / rest : 1;
+    consider(1, k_blocks, 1);
+    for (int strips = 2; strips <= parts && bn / strips >= (narrow ? 64 : 128); strips *= 2) consider(1, k_blocks, strips);
+    const int most = may_split && rest > 0 ? int(std::min<int64_t>({16, k_blocks / 4, parts})) : 1;
+    for (int want = 2; want <= most; ++want) {
+      const int k_split = (k_blocks + want - 1) / want;
+      consider((k_blocks + k_split - 1) / k_split, k_split, 1);
     }
   }
   return best;
 }
 
-void set_tiles(const vsa_plan_s* p, GemmArgs* a, bool may_split) {
-  const Tiling t = tiling(p, a->m_tiles, a->M, a->cols, a->k_blocks, may_split);
+void set_tiles(const vsa_plan_s* p, GemmArgs* a, bool may_split, bool narrow) {
+  const Tiling t = tiling(p, a->m_tiles, a->M, a->cols, a->k_blocks, may_split, narrow);
   a->bn = t.bn;
   a->n_tiles = (a->cols + t.bn - 1) / t.bn;
   a->k_split = t.k_split;
   a->splits = t.splits;
+  a->strips = t.strips;
   a->whole = int(t.whole);
 }
 
@@ -1078,8 +1104,9 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
                   GemmArgs a, bool after, cudaStream_t stream) {
   if (int64_t(a.m_tiles) * a.n_tiles >= (int64_t(1) << 31))
     return fail(VSA_ERR_UNSUPPORTED, "too many output tiles");
-  CUtensorMap ma, mb;
-  if (!map_view(&ma, av, a_box) || !map_view(&mb, bv, b_box))
+  CUtensorMap ma, mb, strip;         // a strip's box of w: a map of its own in the forward product
+  const int strip_box = kOrder == kForward ? b_box / a.strips : b_box;
+  if (!map_view(&ma, av, a_box) || !map_view(&mb, bv, b_box) || !map_view(&strip, bv, strip_box))
     return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
   cudaError_t e = cudaFuncSetAttribute(linear_kernel<kOrder>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
@@ -1093,14 +1120,14 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
   a.by_group = make_div(int64_t(a.m_tiles) * a.group);
   a.by_width = make_div(a.group);
   a.by_last = make_div(a.n_tiles - (a.n_tiles - 1) / a.group * a.group);
-  a.by_splits = make_div(a.splits);
+  a.by_parts = make_div(int64_t(a.splits) * a.strips);
   a.by_rows_b = make_div(a.rows_b);
   a.by_nrow = make_div(a.Nrow);
   a.status = p->d_status;
   a.wait_ns = wait_limit_ns();
-  const int64_t rest = int64_t(a.m_tiles) * a.n_tiles - a.whole, items = a.whole + rest * a.splits;
+  const int64_t rest = int64_t(a.m_tiles) * a.n_tiles - a.whole, items = a.whole + rest * a.splits * a.strips;
   const int grid = 2 * int(std::min<int64_t>(items, pairs_of(p)));
-  e = launch_on(stream, after, linear_kernel<kOrder>, dim3(unsigned(grid)), kThreads, kSmem, ma, mb, a);
+  e = launch_on(stream, after, linear_kernel<kOrder>, dim3(unsigned(grid)), kThreads, kSmem, ma, mb, strip, a);
   if (e == cudaSuccess && a.splits > 1)
     e = launch_on(stream, true, split_join_kernel<kOrder>, dim3(unsigned(rest * (kBM * a.bn / 2048))), 256, 0, a);
   return e == cudaSuccess ? VSA_OK
@@ -1146,7 +1173,7 @@ size_t linear_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
   // tiles and K blocks of either flattening, rows or heads
   const int64_t m1 = (M + kBM - 1) / kBM, m2 = int64_t(B) * ((N + kBM - 1) / kBM);
   const int kb = (C + kBK - 1) / kBK;
-  return std::max(tiling(p, m1, M, O, kb, true).bytes(), tiling(p, m2, M, O, kb, true).bytes());
+  return std::max(tiling(p, m1, M, O, kb, true, true).bytes(), tiling(p, m2, M, O, kb, true, true).bytes());
 }
 
 vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, void* ws, cudaStream_t stream) {
@@ -1161,7 +1188,7 @@ vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, void* ws
   a.N = x.N;
   a.M = x.B * x.N;
   a.cols = q.O;
-  set_tiles(p, &a, ws != nullptr);
+  set_tiles(p, &a, ws != nullptr, true);
   a.partial = static_cast<float*>(ws);
   a.Nrow = q.N;
   a.y = out_view(q.y, q.y_heads, q.O);
@@ -1182,8 +1209,9 @@ size_t linear_backward_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O
   const int64_t k1 = (M + kBK - 1) / kBK, k2 = int64_t(B) * ((N + kBK - 1) / kBK);
   const int ko = (O + kBK - 1) / kBK;
   const int64_t mo = (O + kBM - 1) / kBM;
-  return std::max({tiling(p, m1, M, C, ko, true).bytes(), tiling(p, m2, M, C, ko, true).bytes(),
-                   tiling(p, mo, O, C, int(k1), true).bytes(), tiling(p, mo, O, C, int(k2), true).bytes(),
+  return std::max({tiling(p, m1, M, C, ko, true, false).bytes(), tiling(p, m2, M, C, ko, true, false).bytes(),
+                   tiling(p, mo, O, C, int(k1), true, false).bytes(),
+                   tiling(p, mo, O, C, int(k2), true, false).bytes(),
                    size_t(colsum_runs(M)) * O * sizeof(float)});
 }
 
@@ -1208,7 +1236,7 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.N = g.N;
     a.M = M;
     a.cols = q.C;
-    set_tiles(p, &a, true);
+    set_tiles(p, &a, true, false);
     a.partial = static_cast<float*>(ws);
     a.Nrow = q.N;
     a.y = out_view(q.dx, q.x_heads, q.C);
@@ -1233,7 +1261,7 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.N = g.N;
     a.M = q.O;
     a.cols = q.C;
-    set_tiles(p, &a, true);
+    set_tiles(p, &a, true, false);
     a.Nrow = q.O;
     a.y = OutView{static_cast<uint16_t*>(q.dw), 0, 0, q.C, 31};
     a.partial = static_cast<float*>(ws);
