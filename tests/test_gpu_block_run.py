@@ -220,6 +220,60 @@ def test_streams_and_graphs():
     vsa.vsa_sync_status(c.plan)
 
 
+def test_linears_in_a_row():
+    """Linears that start under the end of the one before, each reading what the last one wrote:
+    on a stream, behind a copy and a memset, and captured on two streams that fork and join."""
+    plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4))
+    x0 = randn(1, 1, 700, 512)
+    ws = [randn(2 + i, 512, 512, scale=0.05) for i in range(4)]
+    bufs = [torch.empty_like(x0) for _ in range(5)]
+    side = torch.cuda.Stream()
+
+    def chain(x, out, scratch, stream=None):
+        """Two buffers in turn, so a linear writes what the one before the last read."""
+        for i, w in enumerate(ws):
+            y = out if i + 1 == len(ws) else scratch[i & 1]
+            x = vsa.vsa_linear(plan, x, w, act="silu", residual=x if i & 1 else None, y=y, stream=stream)
+        return x
+
+    def everything():
+        bufs[0].zero_()
+        chain(x0, bufs[0], bufs[1:3])
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            bufs[3].copy_(bufs[0])
+            chain(bufs[3], bufs[4], [torch.empty_like(x0) for _ in range(2)])
+        chain(bufs[0], bufs[1], [bufs[2], torch.empty_like(x0)])
+        torch.cuda.current_stream().wait_stream(side)
+        return vsa.vsa_linear(plan, bufs[4], ws[0], residual=bufs[1])
+
+    # each linear alone, with a wait after it
+    def alone(x):
+        for i, w in enumerate(ws):
+            y = vsa.vsa_linear(plan, x, w, act="silu", residual=x if i & 1 else None)
+            torch.cuda.synchronize()
+            x = y
+        return x
+
+    once = alone(x0)
+    twice = alone(once)
+    want = vsa.vsa_linear(plan, twice, ws[0], residual=twice)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = everything()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = everything()
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    vsa.vsa_sync_status(plan)
+
+
 def test_repeats_are_bitwise_equal():
     """Sums are taken in a fixed order: two runs give the same bits, the gains' and biases' gradients
     among them, and in split products."""
