@@ -274,6 +274,26 @@ def test_linears_in_a_row():
     vsa.vsa_sync_status(plan)
 
 
+def test_destroyed_during_a_capture():
+    """A plan, a rope and a runner that go while a graph is captured (as a garbage collector may have it)."""
+    plan, gone = (vsa.Plan((4,), (2, 4, 4), (4, 4, 4)) for _ in range(2))
+    rope, gone_rope = vsa.Rope(plan, (16, 24, 24)), vsa.Rope(gone, (16, 24, 24))
+    pipe = vsa.LayerPipeline(plan, 1, 1, 64, 1)
+    x = randn(1, 1, 2, plan.n_tokens, 64)
+    want = vsa.vsa_rope_apply(plan, rope, x)
+    got = torch.empty_like(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gone_rope.close()
+        pipe.close()
+        vsa.vsa_rope_apply(plan, rope, x, got)
+        gone.close()
+    got.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_repeats_are_bitwise_equal():
     """Sums are taken in a fixed order: two runs give the same bits, the gains' and biases' gradients
     among them, and in split products."""

@@ -163,6 +163,7 @@ vsa_status vsa_plan_destroy(vsa_plan p) {
     int prev = -1;
     cudaGetDevice(&prev);
     cudaSetDevice(p->device);
+    const RelaxedCapture relaxed;
     cudaFree(p->d_untile);
     cudaFree(p->d_row_src);
     cudaFree(p->d_block_len);

@@ -235,6 +235,7 @@ void free_rope(vsa_rope_s* r) {
     int prev = -1;
     cudaGetDevice(&prev);
     cudaSetDevice(r->device);
+    const RelaxedCapture relaxed;
     cudaFree(r->d_tab);
     cudaFree(r->d_tok);
     if (prev >= 0) cudaSetDevice(prev);

@@ -203,6 +203,7 @@ vsa_status vsa_runner_elapsed(vsa_runner r, float* ms) {
 
 vsa_status vsa_runner_destroy(vsa_runner r) {
   if (r == nullptr) return VSA_OK;
+  const vsa::RelaxedCapture relaxed;
   cudaStreamSynchronize(r->s_in);
   cudaStreamSynchronize(r->s_comp);
   cudaStreamSynchronize(r->s_out);

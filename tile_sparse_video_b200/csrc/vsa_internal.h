@@ -58,6 +58,19 @@ vsa_status fail(vsa_status code, const std::string& msg);
 // Host planner (plan.cpp).  Fills tables and sizes; returns VSA_OK or VSA_ERR_PLAN.
 vsa_status build_plan(const vsa_geometry& g, vsa_plan_s* p);
 
+// While it lives, frees and waits on this thread leave a stream capture alone that is under way: a
+// garbage collector may destroy a plan at any time.
+class RelaxedCapture {
+ public:
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+  RelaxedCapture(const RelaxedCapture&) = delete;
+  RelaxedCapture& operator=(const RelaxedCapture&) = delete;
+
+ private:
+  cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+};
+
 // Kernel launchers (each .cu file); all asynchronous on `stream`.
 cudaError_t launch_gather_rows(const uint16_t* src, uint16_t* dst, const int32_t* map,
                                int64_t bh, int64_t src_rows, int64_t dst_rows, int D,
