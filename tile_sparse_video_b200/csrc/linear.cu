@@ -80,6 +80,15 @@ __device__ __forceinline__ uint32_t operator/(uint32_t n, const Div& v) {
   return v.d == 1 ? n : __umulhi(n, v.mul) >> v.shift;
 }
 
+// Column sums of dy [B, heads, N, D] -> part [runs][O] in fp32, to be summed in order by
+// colsum_join_kernel.  A unit is 256 columns (32 lanes of 8) of a run of rows.
+struct ColSums {
+  OutView dy;
+  Div by_n, by_cols;               // rows of a batch element; units of 256 columns in a run
+  int M, O, rows, units;           // rows of a run
+  float* part;
+};
+
 struct GemmArgs {
   unsigned int* status;
   unsigned long long wait_ns;      // bound of every wait
@@ -102,6 +111,7 @@ struct GemmArgs {
   int bias_f32, act;
   int add;                         // dgrad: res is added, and not the pre-activation
   float* partial;                  // fp32 [splits][tiles - whole][256][bn]
+  ColSums sum;                     // wgrad: dy's column sums, made on the way (units = 0: not)
 };
 
 // The barrier may be the other CTA's.
@@ -307,6 +317,60 @@ __device__ __forceinline__ uint4* chunk_at(uint8_t* staging, int r, int q) {
   return reinterpret_cast<uint4*>(staging + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
 }
 
+// 16 bytes that are read once: volatile, so that the loads of a step stay ahead of its arithmetic.
+__device__ __forceinline__ uint4 load_once(const uint16_t* p, bool live) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (live)
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+  return v;
+}
+
+// A unit by eight warps with eight rows each in flight; `sync` is a barrier of theirs, and `s`
+// 256 floats a warp, kStride apart.
+constexpr int kColsumRows = 64;
+template <int kStride, class Sync>
+__device__ __forceinline__ void colsum_unit(const ColSums& a, uint32_t unit, int warp, int lane, float* s,
+                                            const Sync& sync) {
+  const uint32_t run = unit / a.by_cols, cols = unit - run * a.by_cols.d;
+  const int col = int(cols) * 256 + 8 * lane;
+  float2 acc[4] = {};
+  const int r0 = int(run) * a.rows, r1 = min(a.M, r0 + a.rows);
+  if (col < a.O) {
+    const uint16_t* base = a.dy.ptr + col_offset(a.dy, col);
+    for (int r = r0 + warp; r < r1; r += kColsumRows) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t ri = r + 8 * i, b = ri / a.by_n;
+        v[i] = load_once(base + b * a.dy.sb + (ri - b * a.by_n.d) * a.dy.sn, int(ri) < r1);
+      }
+      // nothing is added before all eight are asked for
+      asm volatile("" : "+r"(v[0].x), "+r"(v[1].x), "+r"(v[2].x), "+r"(v[3].x), "+r"(v[4].x), "+r"(v[5].x),
+                        "+r"(v[6].x), "+r"(v[7].x));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float2 f[4];
+        unpack(v[i], f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = add2(acc[e], f[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(s + warp * kStride + 8 * lane + 2 * e) = acc[e];
+  sync();
+  const int c = warp * 32 + lane;
+  if (int(cols) * 256 + c < a.O) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += s[w * kStride + c];
+    a.part[int64_t(run) * a.O + cols * 256 + c] = v;
+  }
+  sync();
+}
+
 template <int kOrder>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
@@ -507,6 +571,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* st = staging + (warp - 2) * (32 * 64);
     float* bias = s_bias + (warp - 2) * 128;
     const int row0 = rank * 128 + quad * 32;         // first row of the warp in the tile
+    if (kOrder == kWgrad) {
+      // these warps have nothing else to do during the first products
+      for (uint32_t u = blockIdx.x; u < uint32_t(a.sum.units); u += gridDim.x)
+        colsum_unit<512>(a.sum, u, warp - 2, lane, reinterpret_cast<float*>(staging),
+                         [] { asm volatile("bar.sync 1, 256;" ::: "memory"); });
+    }
     float next_bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // column 32 i + lane of the next tile
     const auto read_bias = [&](int t) {
       int m, n;
@@ -757,16 +827,6 @@ __device__ __forceinline__ void finish(const FewArgs& a, int r, int o, float2 (&
   *at(a.y) = pack_bf16(f[0].x, f[0].y);
 }
 
-// 16 bytes that are read once: volatile, so that the loads of a step stay ahead of its arithmetic.
-__device__ __forceinline__ uint4 load_once(const uint16_t* p, bool live) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (live)
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-  return v;
-}
-
 // kPieces 16-byte pieces of w in flight a lane and step, kPerSm blocks an SM.
 template <int kPieces, int kPerSm>
 __global__ void __launch_bounds__(kFewThreads, kPerSm) linear_few_kernel(const __grid_constant__ FewArgs a) {
@@ -877,51 +937,12 @@ __global__ void __launch_bounds__(256) split_join_kernel(const __grid_constant__
   *at(a.y) = pack(f);
 }
 
-// Column sums of dy [B, heads, N, D] -> fp32 [O]: a block takes 256 columns (32 lanes of 8) of a
-// run of rows, 8 warps side by side with 8 rows each in flight; part[blockIdx.y][O], summed in
-// order by colsum_join_kernel.
-constexpr int kColsumRows = 64;
-
-__global__ void __launch_bounds__(256) colsum_kernel(const OutView dy, const Div by_nrow, int M, int O,
-                                                     int rows_per, float* part) {
-  __shared__ float s[8][256];
+// Column sums by themselves: a block a unit.
+__global__ void __launch_bounds__(256) colsum_kernel(const __grid_constant__ ColSums a) {
+  __shared__ float s[8 * 256];
   let_next_start();
   wait_for_last();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 256 + 8 * lane;
-  float2 acc[4] = {};
-  const int r0 = blockIdx.y * rows_per, r1 = min(M, r0 + rows_per);
-  if (col < O) {
-    const uint16_t* base = dy.ptr + col_offset(dy, col);
-    for (int r = r0 + warp; r < r1; r += kColsumRows) {
-      uint4 v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t ri = r + 8 * i, b = ri / by_nrow;
-        v[i] = load_once(base + b * dy.sb + (ri - b * by_nrow.d) * dy.sn, int(ri) < r1);
-      }
-      // nothing is added before all eight are asked for
-      asm volatile("" : "+r"(v[0].x), "+r"(v[1].x), "+r"(v[2].x), "+r"(v[3].x), "+r"(v[4].x), "+r"(v[5].x),
-                        "+r"(v[6].x), "+r"(v[7].x));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float2 f[4];
-        unpack(v[i], f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = add2(acc[e], f[e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(&s[warp][8 * lane + 2 * e]) = acc[e];
-  __syncthreads();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c < O) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) v += s[w][threadIdx.x];
-    part[int64_t(blockIdx.y) * O + c] = v;
-  }
+  colsum_unit<256>(a, blockIdx.x, threadIdx.x >> 5, threadIdx.x & 31, s, [] { __syncthreads(); });
 }
 
 __global__ void __launch_bounds__(1024) colsum_join_kernel(const float* part, int runs, int O, float* db) {
@@ -1104,6 +1125,20 @@ int colsum_rows(int64_t M) {
 }
 int colsum_runs(int64_t M) { return int(std::max<int64_t>(1, (M + colsum_rows(M) - 1) / colsum_rows(M))); }
 
+ColSums col_sums(const vsa_linear_grad_args& q, float* part) {
+  ColSums a = {};
+  a.dy = out_view(q.dy, q.y_heads, q.O);
+  a.M = int(q.B * q.N);
+  a.O = int(q.O);
+  a.rows = colsum_rows(a.M);
+  const int cols = (a.O + 255) / 256;
+  a.units = cols * colsum_runs(a.M);
+  a.by_n = make_div(q.N);
+  a.by_cols = make_div(cols);
+  a.part = part;
+  return a;
+}
+
 template <int kOrder>
 vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv, int b_box,
                   GemmArgs a, cudaStream_t stream) {
@@ -1207,17 +1242,17 @@ vsa_status launch_linear(const vsa_plan_s* p, const vsa_linear_args& q, void* ws
 
 size_t linear_backward_bytes(const vsa_plan_s* p, int B, int64_t N, int C, int O) {
   if (int64_t(B) * N == 0) return 0;
-  // one buffer, used in turn by the products' partial sums and the column sums; tiles and K blocks of
-  // either flattening, rows or heads
+  // one buffer, used in turn by the products' partial sums, the column sums behind those of
+  // dw; tiles and K blocks of either flattening, rows or heads
   const int64_t M = int64_t(B) * N;
   const int64_t m1 = (M + kBM - 1) / kBM, m2 = int64_t(B) * ((N + kBM - 1) / kBM);
   const int64_t k1 = (M + kBK - 1) / kBK, k2 = int64_t(B) * ((N + kBK - 1) / kBK);
   const int ko = (O + kBK - 1) / kBK;
   const int64_t mo = (O + kBM - 1) / kBM;
   return std::max({tiling(p, m1, M, C, ko, true, false).bytes(), tiling(p, m2, M, C, ko, true, false).bytes(),
-                   tiling(p, mo, O, C, int(k1), true, false).bytes(),
-                   tiling(p, mo, O, C, int(k2), true, false).bytes(),
-                   size_t(colsum_runs(M)) * O * sizeof(float)});
+                   std::max(tiling(p, mo, O, C, int(k1), true, false).bytes(),
+                            tiling(p, mo, O, C, int(k2), true, false).bytes()) +
+                       size_t(colsum_runs(M)) * O * sizeof(float)});
 }
 
 vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_args& q, void* ws,
@@ -1251,6 +1286,11 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     const vsa_status st = launch<kDgrad>(p, g, 128, matrix(q.w, q.O, q.C), kBK, a, stream);
     if (st != VSA_OK) return st;
   }
+  float* sums = static_cast<float*>(ws);           // column sums, behind dw's partial sums
+  // The product for dw takes the column sums along where it reads dy for more than one tile of
+  // columns: 9,772 x 1,024 -> 1,024 (dx, dw, db) 52 -> 46.4 us, 33,920 x 512 -> 1,024 (dw, db) 55.3 -> 50.6.
+  // With one there is too little to hide them under: 33,920 x 64 -> 7,168 168 us apart, 186 along.
+  const bool along = q.dw != nullptr && q.db != nullptr && q.C > 256;
   if (q.dw != nullptr) {
     View g = dy, x = make_view(q.x, q.B, q.N, q.x_heads, q.C);
     if (rows_even(g) && rows_even(x)) {
@@ -1270,18 +1310,21 @@ vsa_status launch_linear_backward(const vsa_plan_s* p, const vsa_linear_grad_arg
     a.Nrow = q.O;
     a.y = OutView{static_cast<uint16_t*>(q.dw), 0, 0, q.C, 31};
     a.partial = static_cast<float*>(ws);
+    if (along) {
+      const int64_t rest = int64_t(a.m_tiles) * a.n_tiles - a.whole;
+      sums += a.splits > 1 ? a.splits * rest * kBM * a.bn : 0;
+      a.sum = col_sums(q, sums);
+    }
     const vsa_status st = launch<kWgrad>(p, g, kBK, x, kBK, a, stream);
     if (st != VSA_OK) return st;
   }
   if (q.db != nullptr) {
-    const int runs = colsum_runs(M);
-    float* sums = static_cast<float*>(ws);
-    cudaError_t e = launch_on(stream, colsum_kernel, dim3(unsigned((q.O + 255) / 256), unsigned(runs)), 256,
-                              0, out_view(q.dy, q.y_heads, q.O), make_div(q.N), int(M), int(q.O),
-                              colsum_rows(M), sums);
+    const ColSums a = col_sums(q, sums);
+    cudaError_t e = cudaSuccess;
+    if (!along) e = launch_on(stream, colsum_kernel, dim3(unsigned(a.units)), 256, 0, a);
     if (e == cudaSuccess)
       e = launch_on(stream, colsum_join_kernel, dim3(unsigned((q.O + 31) / 32)), 1024, 0,
-                    static_cast<const float*>(sums), runs, int(q.O), q.db);
+                    static_cast<const float*>(sums), colsum_runs(M), int(q.O), q.db);
     if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
   }
   return VSA_OK;
