@@ -24,6 +24,7 @@
 // two heads of 366 tokens 4 us (launch).  A warp per tile and head with its loads in registers, which
 // looked the angles up for every row and head, took 2,031, 252, 815, 39 and 8 us.
 #include <algorithm>
+#include <cmath>
 
 #include "block_internal.h"
 #include "sm100.cuh"
@@ -198,8 +199,9 @@ struct Block {
 // Heads in flight.  With two the tiles take 1,125 us in place of 1,101; with four only one block of
 // the backward fits an SM (550 us in place of 460).
 constexpr int kStages = 3;
-// Heads of a tile item, at most: its column sums (4 KB a head of 128 channels, 64 KB) and the slots
-// (48 KB) leave room for two blocks on an SM.
+// Heads of an item of the forward, at most.  Tiles: their column sums (4 KB a head of 128 channels,
+// 64 KB) and the slots (48 KB) leave room for two blocks on an SM.  Natural order: 42 x 33,920 take 116.7 us
+// with 14, 118.7 with 21 and 123.6 with all heads an item.
 constexpr int kMaxGroup = 16;
 constexpr int kGradRows = 64;         // rows of an item of the backward
 
@@ -465,22 +467,27 @@ RopeArgs rope_args(const vsa_rope_s* r, int inverse) {
   return a;
 }
 
-// Heads of an item.  An item costs its heads and a start of about two more (its rows' indices and
-// angles, and the first heads' way from memory); the blocks come in waves of `slots`: the
-// group that makes the waves shortest.  (One head an item: small layer 41 us, eight: 27 us; all 42 heads
-// an item or a sixteenth of the waves: 1,186 and 1,318 us at 104,704 tokens.)
+// Heads of an item, at most max_group: an item costs its heads and a start of about two more (its
+// rows' indices and angles, and the first heads' way from memory).  Two blocks an SM with
+// their items in step come in waves of `slots`: the group that makes the waves shortest (one head an
+// item: small layer 41 us, eight: 27 us; all 42 heads an item or a sixteenth of the waves: 1,186 and
+// 1,318 us at 104,704 tokens).  Six (natural order) share the memory whatever the wave, and the
+// last items cost a third of their heads: Q and K of 8 x 9,772 36.2, 24.6, 19.2 and 17.1 us with one, two,
+// four and eight heads an item (by whole waves it would be four), 42 x 700 15.3 with one, 8.7
+// with six and 16.0 with 42.
 template <class Args>
 bool set_items(Args* a, const vsa_plan_s* p, int64_t row_blocks, int B, int H, int n, int64_t slots,
-               int max_group, int64_t* items) {
+               int max_group, bool in_step, int64_t* items) {
   a->row_src = p->d_row_src;
   a->H = H;
   a->T = int(row_blocks);
-  int64_t best = -1;
+  double least = 1e300;
   for (int g = 1; g <= std::min(H, max_group); ++g) {
     const int64_t groups = (H + g - 1) / g;
-    const int64_t cost = (int64_t(B) * row_blocks * n * groups + slots - 1) / slots * (g + 2);
-    if (best < 0 || cost < best) {
-      best = cost;
+    const double waves = double(int64_t(B) * row_blocks * n * groups) / double(slots);
+    const double cost = in_step ? std::ceil(waves) * (g + 2) : waves * (g + 2.3) + 0.35 * g;
+    if (cost < least) {
+      least = cost;
       a->group = g;
       a->groups = int(groups);
     }
@@ -517,8 +524,7 @@ vsa_status launch_norm_rope(const vsa_plan_s* p, const vsa_rope_s* rope, const H
   const int64_t row_blocks = tiled ? p->n_tiles : (p->n_tokens + 2048 / D - 1) / (2048 / D);
   a.R = p->R;
   int64_t items = 0;
-  if (!set_items(&a, p, row_blocks, B, H, n, int64_t(sms(p)) * (tiled ? 2 : 6),
-                 tiled ? kMaxGroup : H, &items))
+  if (!set_items(&a, p, row_blocks, B, H, n, int64_t(sms(p)) * (tiled ? 2 : 6), kMaxGroup, tiled, &items))
     return fail(VSA_ERR_UNSUPPORTED, "too many heads and rows for one launch");
   const bool halves = rope != nullptr && rope->halves;
   cudaError_t e;
@@ -565,7 +571,7 @@ vsa_status launch_norm_rope_backward(const vsa_plan_s* p, const vsa_rope_s* rope
   a.partial = static_cast<float*>(ws);
   a.rows = tiled ? p->n_padded : p->n_tokens;
   int64_t items = 0;
-  if (!set_items(&a, p, (a.rows + kGradRows - 1) / kGradRows, B, H, n, max_blocks(p), H, &items))
+  if (!set_items(&a, p, (a.rows + kGradRows - 1) / kGradRows, B, H, n, max_blocks(p), H, true, &items))
     return fail(VSA_ERR_UNSUPPORTED, "too many heads and rows for one launch");
   a.n_items = unsigned(items);
   const int64_t blocks = std::min<int64_t>(items, max_blocks(p));
