@@ -220,9 +220,10 @@ def test_streams_and_graphs():
     vsa.vsa_sync_status(c.plan)
 
 
-def test_linears_in_a_row():
+@pytest.mark.parametrize("copied", [True, False])
+def test_linears_in_a_row(copied):
     """Linears that start under the end of the one before, each reading what the last one wrote:
-    on a stream, behind a copy and a memset, and captured on two streams that fork and join."""
+    on a stream, behind a copy, a memset or an event alone, and captured on two streams that fork and join."""
     plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4))
     x0 = randn(1, 1, 700, 512)
     ws = [randn(2 + i, 512, 512, scale=0.05) for i in range(4)]
@@ -241,8 +242,9 @@ def test_linears_in_a_row():
         chain(x0, bufs[0], bufs[1:3])
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            bufs[3].copy_(bufs[0])
-            chain(bufs[3], bufs[4], [torch.empty_like(x0) for _ in range(2)])
+            if copied:
+                bufs[3].copy_(bufs[0])
+            chain(bufs[3] if copied else bufs[0], bufs[4], [torch.empty_like(x0) for _ in range(2)])
         chain(bufs[0], bufs[1], [bufs[2], torch.empty_like(x0)])
         torch.cuda.current_stream().wait_stream(side)
         return vsa.vsa_linear(plan, bufs[4], ws[0], residual=bufs[1])

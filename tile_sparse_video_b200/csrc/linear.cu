@@ -27,8 +27,9 @@
 // TFLOP/s, the library's plain product of the same operands 1.65-1.9 ms in the same runs; gradients 1.75-2.1
 // ms each.  The tensor pipe is active 99 % of the time (ncu) at the 1.1-1.25 GHz to which the 1 kW cap takes the
 // clock: power bounds it.  2,048 x 5,376 x 5,376: 86 us forward, 77 us weight gradient (library 86-88 and 79).
-// 9,772 x 1,024 -> 1,024 18.8 us (library 18.7), with bias and residual 21.7.  On the way: one lane on the producer's and issuer's loops with divisions
-// in them 1,050-1,250 TFLOP/s, whole warps without divisions 1,400-1,500; branches for every eight values and
+// 9,772 x 1,024 -> 1,024 18.8 us (library 18.7), with bias and residual 21.7.  On the way: one lane on the
+// producer's and issuer's loops with divisions in them 1,050-1,250 TFLOP/s, whole warps without
+// divisions 1,400-1,500; branches for every eight values and
 // scalar arithmetic in the epilogue 45 us in place of 34 (4,096 x 1,024 -> 4,096, GELU); cluster-scope
 // releases, which wait for a warp's stores, another 2 us.
 #include <algorithm>
@@ -336,7 +337,7 @@ __device__ __forceinline__ void colsum_unit(const ColSums& a, uint32_t unit, int
   const uint32_t run = unit / a.by_cols, cols = unit - run * a.by_cols.d;
   const int col = int(cols) * 256 + 8 * lane;
   float2 acc[4] = {};
-  const int r0 = int(run) * a.rows, r1 = min(a.M, r0 + a.rows);
+  const int r0 = int(run) * a.rows, r1 = int(min(uint32_t(a.M), uint32_t(r0) + uint32_t(a.rows)));
   if (col < a.O) {
     const uint16_t* base = a.dy.ptr + col_offset(a.dy, col);
     for (int r = r0 + warp; r < r1; r += kColsumRows) {
@@ -1087,7 +1088,8 @@ Tiling tiling(const vsa_plan_s* p, int64_t m_tiles, int64_t M, int cols, int k_b
     const double idle = std::max(waves * P, done - std::max(P, E));
     const auto consider = [&](int splits, int k_split, int strips) {
       const int width = bn / strips;
-      const double join = splits > 1 ? 1.0 + double(splits) * double(rest) * double(std::min<int64_t>(M, kBM)) * bn * 8 / 4e6 : 0.0;
+      const double sums = double(splits) * double(rest) * double(std::min<int64_t>(M, kBM)) * bn * 8;
+      const double join = splits > 1 ? 1.0 + sums / 4e6 : 0.0;
       const double t = rest > 0 ? std::max(done, idle + products(width, k_split)) + epilogue(width) + join : done;
       if (t < least) {
         least = t;
@@ -1096,7 +1098,8 @@ Tiling tiling(const vsa_plan_s* p, int64_t m_tiles, int64_t M, int cols, int k_b
     };
     const int64_t parts = rest > 0 ? pairs_of(p) / rest : 1;
     consider(1, k_blocks, 1);
-    for (int strips = 2; strips <= parts && bn / strips >= (narrow ? 64 : 128); strips *= 2) consider(1, k_blocks, strips);
+    for (int strips = 2; strips <= parts && bn / strips >= (narrow ? 64 : 128); strips *= 2)
+      consider(1, k_blocks, strips);
     const int most = may_split && rest > 0 ? int(std::min<int64_t>({16, k_blocks / 4, parts})) : 1;
     for (int want = 2; want <= most; ++want) {
       const int k_split = (k_blocks + want - 1) / want;

@@ -19,8 +19,8 @@
 //
 // Measured (B200, device time, share of the measured 6,549 GB/s copy rate): Q, K and V of 104,704
 // tokens x 42 heads into tiles with their means 1,092 us (6.81 GB, 95 %); the rotation alone of 33,920 x 42 on
-// a [B,N,H,D] tensor 116 us (96 %); the backward of Q, K and V there 460 us (97 %); Q and K of 9,772
-// x 8 out of one [B,N,3,H,D] projection 19.7 us (80 MB, 62 %: start and end of so short a kernel);
+// a [B,N,H,D] tensor 114 us (97 %); the backward of Q, K and V there 460 us (97 %); Q and K of 9,772
+// x 8 out of one [B,N,3,H,D] projection 17.1 us (80 MB, 71 %: start and end of so short a kernel);
 // two heads of 366 tokens 4 us (launch).  A warp per tile and head with its loads in registers, which
 // looked the angles up for every row and head, took 2,031, 252, 815, 39 and 8 us.
 #include <algorithm>
