@@ -1,0 +1,100 @@
+"""Calls from two host threads at once, each with its own plan, stream, buffers and sizes: what one
+call asks of a kernel (its shared memory among it) stays its own.  The threads are C's, and do
+nothing between their calls."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+from tests.test_gpu_block import randn
+from tile_sparse_video_b200 import vsa
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+THREADS = r'''
+#include <pthread.h>
+#include <string.h>
+#include "vsa_block.h"
+typedef struct {
+  vsa_plan plan; vsa_rope rope; const vsa_head_tensor* item; int H, D, rounds; void* stream;
+  int bad; pthread_barrier_t* gate; char said[120];
+} job;
+static void count(job* j, vsa_status st) {
+  if (st != VSA_OK && !j->bad++) strncpy(j->said, vsa_last_error(), sizeof j->said - 1);
+}
+static void* tiles(void* p) {
+  job* j = p;
+  pthread_barrier_wait(j->gate);
+  for (int i = 0; i < j->rounds; ++i)
+    count(j, vsa_norm_rope_permute_pool(j->plan, j->rope, j->item, 1, 1e-6f, 1, j->H, j->D, j->stream));
+  return 0;
+}
+int run(job* jobs, int n) {
+  pthread_t t[8];
+  pthread_barrier_t gate;
+  pthread_barrier_init(&gate, 0, n);
+  for (int i = 0; i < n; ++i) {
+    jobs[i].gate = &gate;
+    if (pthread_create(&t[i], 0, tiles, &jobs[i])) return -1;
+  }
+  for (int i = 0; i < n; ++i) pthread_join(t[i], 0);
+  return 0;
+}
+'''
+P = ctypes.c_void_p
+
+
+class Job(ctypes.Structure):
+    _fields_ = [("plan", P), ("rope", P), ("item", P), ("H", ctypes.c_int), ("D", ctypes.c_int),
+                ("rounds", ctypes.c_int), ("stream", P), ("bad", ctypes.c_int), ("gate", P),
+                ("said", ctypes.c_char * 120)]
+
+
+@pytest.fixture(scope="module")
+def threads(libvsa, tmp_path_factory):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+    d = tmp_path_factory.mktemp("threads")
+    (d / "threads.c").write_text(THREADS)
+    where = os.path.join(ROOT, "tile_sparse_video_b200")
+    subprocess.run(["gcc", "-O1", "-shared", "-fPIC", "-I", os.path.join(ROOT, "include"), str(d / "threads.c"),
+                    "-o", str(d / "threads.so"), "-L", where, "-l:libvsa.so", "-Wl,-rpath," + where, "-lpthread"],
+                   check=True)
+    run = ctypes.CDLL(str(d / "threads.so")).run
+    run.argtypes, run.restype = [P, ctypes.c_int], ctypes.c_int
+
+    def refused(jobs):
+        """(calls that were refused, what the first of them said) of each thread."""
+        jobs = (Job * len(jobs))(*jobs)
+        assert run(jobs, len(jobs)) == 0
+        return [(j.bad, j.said) for j in jobs]
+    yield refused
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("D,heads", [(64, (440, 600)), (128, (80, 300))])
+def test_norm_rope_permute_pool(threads, D, heads):
+    """Items of other numbers of heads, so other sizes of shared memory for one kernel, each of them
+    above what a kernel may take without leave."""
+    jobs, checks, keep = [], [], []
+    for i, H in enumerate(heads):
+        plan = vsa.Plan((9, 70), (4, 8, 8), (4, 4, 4))
+        rope, stream = vsa.Rope(plan, (24, 20, 20)), torch.cuda.Stream()
+        x = randn(i, 1, H, plan.n_tokens, D)
+        (want, means), = vsa.vsa_norm_rope_permute_pool(plan, [vsa.HeadTensor(x)], rope)
+        y, m = torch.empty_like(want), torch.empty_like(means)
+        item = ctypes.create_string_buffer(vsa._HEAD_TENSOR.pack(
+            *vsa._view(plan, x, "x", x.shape), 0, 0, 1, 1, y.data_ptr(), 0, 0, 0, m.data_ptr()))
+        jobs.append(Job(plan.handle, rope.handle, ctypes.addressof(item), H, D, 20000, stream.cuda_stream))
+        checks.append((plan, y, want, m, means))
+        keep.append((rope, stream, x, item))
+    torch.cuda.synchronize()
+    assert threads(jobs) == [(0, b"")] * 2
+    torch.cuda.synchronize()
+    for plan, y, want, m, means in checks:
+        vsa.vsa_sync_status(plan)
+        assert torch.equal(y, want) and torch.equal(m, means)

@@ -496,12 +496,15 @@ bool set_items(Args* a, const vsa_plan_s* p, int64_t row_blocks, int B, int H, i
   return *items < (int64_t(1) << 31) && row_blocks < (int64_t(1) << 31);
 }
 
+// smem: this call's shared memory; most: the most that any call of the kernel takes.  The leave is the
+// function's, not the call's: every thread asks for the same, so that none takes from another's
+// between its leave and its launch.
 template <class Kernel, class Args>
-cudaError_t launch(Kernel k, int64_t items, int n, int threads, uint32_t smem, const Args& a,
+cudaError_t launch(Kernel k, int64_t items, int n, int threads, uint32_t smem, uint32_t most, const Args& a,
                    cudaStream_t stream) {
   // 48 KB need no leave, less the 4 KB a kernel has besides
-  if (smem > 44 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (most > 44 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
     if (e != cudaSuccess) return e;
   }
   k<<<dim3(unsigned(items), unsigned(n)), threads, smem, stream>>>(a);
@@ -531,9 +534,10 @@ vsa_status launch_norm_rope(const vsa_plan_s* p, const vsa_rope_s* rope, const H
 #define VSA_LAUNCH(DD, TL, U)                                                                     \
   {                                                                                               \
     static_assert(Block<DD, 256, U>::kRows == (TL ? 64 : 2048 / DD), "rows of a pass or an item"); \
-    const uint32_t smem = kStages * Block<DD, 256, U>::kStage + (TL ? a.group * 8 * DD * 4 : 0);  \
-    e = halves ? launch(norm_rope_kernel<DD, true, TL, 256, U>, items, n, 256, smem, a, stream)   \
-               : launch(norm_rope_kernel<DD, false, TL, 256, U>, items, n, 256, smem, a, stream); \
+    const uint32_t rows = kStages * Block<DD, 256, U>::kStage, head = TL ? 8 * DD * 4 : 0;        \
+    const uint32_t smem = rows + a.group * head, most = rows + kMaxGroup * head;                  \
+    e = halves ? launch(norm_rope_kernel<DD, true, TL, 256, U>, items, n, 256, smem, most, a, stream)   \
+               : launch(norm_rope_kernel<DD, false, TL, 256, U>, items, n, 256, smem, most, a, stream); \
   }
   if (D == 128) {
     if (tiled)
@@ -582,9 +586,9 @@ vsa_status launch_norm_rope_backward(const vsa_plan_s* p, const vsa_rope_s* rope
     static_assert(Block<DD, 256, U>::kRows == kGradRows, "rows of an item");                  \
     const uint32_t smem = 2 * kStages * Block<DD, 256, U>::kStage;                            \
     e = halves ? launch(norm_rope_backward_kernel<DD, true, TL, 256, U>, blocks, n, 256,      \
-                        smem, a, stream)                                                      \
+                        smem, smem, a, stream)                                                \
                : launch(norm_rope_backward_kernel<DD, false, TL, 256, U>, blocks, n, 256,     \
-                        smem, a, stream);                                                     \
+                        smem, smem, a, stream);                                               \
   }
   if (D == 128) {
     if (tiled)
