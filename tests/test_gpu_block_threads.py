@@ -1,9 +1,10 @@
-"""Calls from two host threads at once, each with its own plan, stream, buffers and sizes: what one
-call asks of a kernel (its shared memory among it) stays its own.  The threads are C's, and do
-nothing between their calls."""
+"""Calls from host threads.  Two at once, each with its own plan, stream, buffers and sizes: what one
+call asks of a kernel (its shared memory among it) stays its own; these threads are C's, and do
+nothing between their calls.  And a thread whose first work with the GPU is the call itself."""
 import ctypes
 import os
 import subprocess
+import threading
 
 import pytest
 import torch
@@ -98,3 +99,45 @@ def test_norm_rope_permute_pool(threads, D, heads):
     for plan, y, want, m, means in checks:
         vsa.vsa_sync_status(plan)
         assert torch.equal(y, want) and torch.equal(m, means)
+
+
+def test_first_call_of_a_thread(threads):
+    """Products of every kind from threads that have not yet touched the GPU."""
+    plan = vsa.Plan((9, 70), (4, 8, 8), (4, 4, 4))
+    n, C, H, D, k = plan.n_tokens, 256, 2, 128, 1
+    s = torch.cuda.Stream()
+    x, w = randn(1, 1, n, C), randn(2, H * D, C, scale=0.05)
+    heads = [randn(3 + i, 1, H, n, D) for i in range(4)]
+    layer = vsa.TrainingLayer(plan, 1, H, D, k)
+    outs = [torch.empty(1, n, H * D, dtype=torch.bfloat16, device="cuda"),
+            torch.empty(1, H, n, D, dtype=torch.bfloat16, device="cuda")]
+    ws = torch.empty(max(vsa._workspace_bytes(plan, "vsa_linear_workspace_size", 1, n, C, H * D), 16),
+                     dtype=torch.uint8, device="cuda")
+    grads = (torch.empty_like(x), torch.empty_like(w), torch.empty(H * D, device="cuda"))
+    bws = vsa.linear_backward_workspace(plan, 1, n, C, H * D)
+    calls = {
+        "linear": lambda st: [vsa.vsa_linear(plan, x, w, y=outs[0], ws=ws, stream=st)],
+        "linear backward": lambda st: list(vsa.vsa_linear_backward(
+            plan, heads[0], x, w, dx=grads[0], dw=grads[1], db=grads[2], ws=bws, stream=st)),
+        "project": lambda st: [vsa.vsa_project(plan, x, w, H, D, y=outs[1], stream=st)],
+        "layer": lambda st: [layer.forward(*heads, stream=st)],
+        "layer backward": lambda st: list(layer.backward(heads[0], stream=st)),
+    }
+    for name, call in calls.items():
+        want = [t.clone() for t in call(s)]
+        s.synchronize()
+        got, errors = [], []
+
+        def work():
+            try:
+                got.extend(call(s))
+            except Exception as e:
+                errors.append(e)
+        t = threading.Thread(target=work)
+        torch.cuda.synchronize()
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not errors, (name, errors)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+    vsa.vsa_sync_status(plan)

@@ -1021,10 +1021,8 @@ void flatten(View* v) {
   v->B = 1;
 }
 
-// TMA map of a view, box 64 channels x box_rows rows, 128-byte swizzle.
+// TMA map of a view, box 64 channels x box_rows rows.
 bool map_view(CUtensorMap* m, const View& v, int box_rows) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (enc == nullptr) return false;
   const cuuint64_t dims[4] = {cuuint64_t(v.D), cuuint64_t(v.N), cuuint64_t(v.H), cuuint64_t(v.B)};
   // the stride of a dimension of extent 1 is not used, but has to be valid
   const auto bytes = [](int64_t extent, int64_t stride) {
@@ -1032,10 +1030,7 @@ bool map_view(CUtensorMap* m, const View& v, int box_rows) {
   };
   const cuuint64_t strides[3] = {bytes(v.N, v.sn), bytes(v.H, v.sh), bytes(v.B, v.sb)};
   const cuuint32_t box[4] = {64u, cuuint32_t(box_rows), 1u, 1u};
-  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(v.ptr), dims, strides,
-             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, v.ptr, 4, dims, strides, box);
 }
 
 View matrix(const void* p, int64_t rows, int cols) {

@@ -252,18 +252,31 @@ inline EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-// 2-D map over a [rows, D] bf16 matrix (row stride D elements), box = 64
-// columns x box_rows rows, 128-byte swizzle; out-of-range elements load as 0.
-inline bool make_map(CUtensorMap* m, const void* ptr, int64_t rows, int D, int box_rows) {
+// Map of a bf16 tensor in boxes of 64 columns, 128-byte swizzle; out-of-range elements load as 0.
+// The driver encodes only for a thread with a context, and a host thread's first call may be this
+// one: it then takes its device's, and the encoding is tried again.
+inline bool encode_map(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn enc = get_encode_fn();
   if (enc == nullptr) return false;
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const auto encode = [&] {
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(ptr), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  int device = 0;
+  return cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess && encode();
+}
+
+// 2-D map over a [rows, D] bf16 matrix (row stride D elements), box = 64
+// columns x box_rows rows.
+inline bool make_map(CUtensorMap* m, const void* ptr, int64_t rows, int D, int box_rows) {
   const cuuint64_t dims[2] = {cuuint64_t(D), cuuint64_t(rows)};
   const cuuint64_t strides[1] = {cuuint64_t(D) * 2};
   const cuuint32_t box[2] = {64u, cuuint32_t(box_rows)};
-  const cuuint32_t estr[2] = {1u, 1u};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, ptr, 2, dims, strides, box);
 }
 
 }  // namespace sm100
