@@ -109,23 +109,24 @@ def test_first_call_of_a_thread(threads):
     x, w = randn(1, 1, n, C), randn(2, H * D, C, scale=0.05)
     heads = [randn(3 + i, 1, H, n, D) for i in range(4)]
     layer = vsa.TrainingLayer(plan, 1, H, D, k)
-    outs = [torch.empty(1, n, H * D, dtype=torch.bfloat16, device="cuda"),
-            torch.empty(1, H, n, D, dtype=torch.bfloat16, device="cuda")]
+    rows, by_head = (torch.empty(shape, dtype=torch.bfloat16, device="cuda") for shape in ((1, n, H * D), (1, H, n, D)))
     ws = torch.empty(max(vsa._workspace_bytes(plan, "vsa_linear_workspace_size", 1, n, C, H * D), 16),
                      dtype=torch.uint8, device="cuda")
     grads = (torch.empty_like(x), torch.empty_like(w), torch.empty(H * D, device="cuda"))
     bws = vsa.linear_backward_workspace(plan, 1, n, C, H * D)
     calls = {
-        "linear": lambda st: [vsa.vsa_linear(plan, x, w, y=outs[0], ws=ws, stream=st)],
+        "linear": lambda st: [vsa.vsa_linear(plan, x, w, y=rows, ws=ws, stream=st)],
         "linear backward": lambda st: list(vsa.vsa_linear_backward(
             plan, heads[0], x, w, dx=grads[0], dw=grads[1], db=grads[2], ws=bws, stream=st)),
-        "project": lambda st: [vsa.vsa_project(plan, x, w, H, D, y=outs[1], stream=st)],
+        "project": lambda st: [vsa.vsa_project(plan, x, w, H, D, y=by_head, stream=st)],
         "layer": lambda st: [layer.forward(*heads, stream=st)],
         "layer backward": lambda st: list(layer.backward(heads[0], stream=st)),
     }
     for name, call in calls.items():
-        want = [t.clone() for t in call(s)]
+        torch.cuda.synchronize()
+        res = call(s)
         s.synchronize()
+        want = [t.clone() for t in res]
         got, errors = [], []
 
         def work():
