@@ -21,6 +21,8 @@ THREADS = r'''
 #include "vsa_block.h"
 typedef struct {
   vsa_plan plan; vsa_rope rope; const vsa_head_tensor* item; int H, D, rounds; void* stream;
+  const void *q, *k, *v; const int32_t* topk; void* out;
+  const void* d_out; const float *lse, *delta; void *dq, *dk, *dv, *ws; size_t ws_bytes; int n_ref;
   int bad; pthread_barrier_t* gate; char said[120];
 } job;
 static void count(job* j, vsa_status st) {
@@ -33,13 +35,30 @@ static void* tiles(void* p) {
     count(j, vsa_norm_rope_permute_pool(j->plan, j->rope, j->item, 1, 1e-6f, 1, j->H, j->D, j->stream));
   return 0;
 }
-int run(job* jobs, int n) {
+static void* attention(void* p) {
+  job* j = p;
+  pthread_barrier_wait(j->gate);
+  for (int i = 0; i < j->rounds; ++i)
+    count(j, vsa_sparse_attn(j->plan, j->q, j->k, j->v, j->topk, 1, j->H, j->D, 1, 0.1f, j->out, 0, 0, 0,
+                             j->stream));
+  return 0;
+}
+static void* backward(void* p) {
+  job* j = p;
+  pthread_barrier_wait(j->gate);
+  for (int i = 0; i < j->rounds; ++i)
+    count(j, vsa_sparse_attn_backward(j->plan, j->q, j->k, j->v, j->d_out, j->topk, 1, 0, j->n_ref, j->lse, j->delta,
+                                      0, 0, 0, 1, j->H, j->D, 0.1f, j->dq, j->dk, j->dv, j->ws, j->ws_bytes,
+                                      j->stream));
+  return 0;
+}
+int run(job* jobs, int n, int what) {
   pthread_t t[8];
   pthread_barrier_t gate;
   pthread_barrier_init(&gate, 0, n);
   for (int i = 0; i < n; ++i) {
     jobs[i].gate = &gate;
-    if (pthread_create(&t[i], 0, tiles, &jobs[i])) return -1;
+    if (pthread_create(&t[i], 0, what == 2 ? backward : what == 1 ? attention : tiles, &jobs[i])) return -1;
   }
   for (int i = 0; i < n; ++i) pthread_join(t[i], 0);
   return 0;
@@ -50,7 +69,9 @@ P = ctypes.c_void_p
 
 class Job(ctypes.Structure):
     _fields_ = [("plan", P), ("rope", P), ("item", P), ("H", ctypes.c_int), ("D", ctypes.c_int),
-                ("rounds", ctypes.c_int), ("stream", P), ("bad", ctypes.c_int), ("gate", P),
+                ("rounds", ctypes.c_int), ("stream", P), ("q", P), ("k", P), ("v", P), ("topk", P), ("out", P),
+                ("d_out", P), ("lse", P), ("delta", P), ("dq", P), ("dk", P), ("dv", P), ("ws", P),
+                ("ws_bytes", ctypes.c_size_t), ("n_ref", ctypes.c_int), ("bad", ctypes.c_int), ("gate", P),
                 ("said", ctypes.c_char * 120)]
 
 
@@ -66,12 +87,12 @@ def threads(libvsa, tmp_path_factory):
                     "-o", str(d / "threads.so"), "-L", where, "-l:libvsa.so", "-Wl,-rpath," + where, "-lpthread"],
                    check=True)
     run = ctypes.CDLL(str(d / "threads.so")).run
-    run.argtypes, run.restype = [P, ctypes.c_int], ctypes.c_int
+    run.argtypes, run.restype = [P, ctypes.c_int, ctypes.c_int], ctypes.c_int
 
-    def refused(jobs):
+    def refused(jobs, what):
         """(calls that were refused, what the first of them said) of each thread."""
         jobs = (Job * len(jobs))(*jobs)
-        assert run(jobs, len(jobs)) == 0
+        assert run(jobs, len(jobs), what) == 0
         return [(j.bad, j.said) for j in jobs]
     yield refused
     torch.cuda.synchronize()
@@ -94,11 +115,48 @@ def test_norm_rope_permute_pool(threads, D, heads):
         checks.append((plan, y, want, m, means))
         keep.append((rope, stream, x, item))
     torch.cuda.synchronize()
-    assert threads(jobs) == [(0, b"")] * 2
+    assert threads(jobs, 0) == [(0, b"")] * 2
     torch.cuda.synchronize()
     for plan, y, want, m, means in checks:
         vsa.vsa_sync_status(plan)
         assert torch.equal(y, want) and torch.equal(m, means)
+
+
+@pytest.mark.parametrize("tile", [(4, 4, 4), (4, 8, 4)], ids=["r64", "r128"])
+@pytest.mark.parametrize("what", [1, 2], ids=["forward", "backward"])
+def test_attention(threads, tile, what):
+    """The attention kernels' lists grow with the tiles: plans of few and of many."""
+    jobs, checks, keep = [], [], []
+    for i, prefix in enumerate(((70,), (70,) * 60)):
+        plan, stream = vsa.Plan(prefix, (4, 8, 8), tile), torch.cuda.Stream()
+        q, k, v, g = (randn(10 * i + s, 1, 1, plan.n_padded, 128) for s in range(4))
+        topk = torch.full((1, 1, plan.n_video_tiles, 1), plan.n_prefix_tiles, dtype=torch.int32, device="cuda")
+        out, lse = vsa.vsa_sparse_attn(plan, q, k, v, topk, 1, 0.1, want_lse=True)
+        job = Job(plan.handle, None, None, 1, 128, 20000 if what == 1 else 4000, stream.cuda_stream, q.data_ptr(),
+                  k.data_ptr(), v.data_ptr(), topk.data_ptr())
+        if what == 1:
+            want, got = [out], [torch.empty_like(out)]
+            job.out = got[0].data_ptr()
+            extra = ()
+        else:
+            ws = torch.empty(vsa.vsa_backward_workspace_size(plan, 1, 1, 128), dtype=torch.uint8, device="cuda")
+            delta = (out.float() * g.float()).sum(-1)
+            want = vsa.vsa_sparse_attn_backward(plan, q, k, v, g, topk, 1, lse, delta, ws, scale=0.1)
+            got = [torch.empty_like(t) for t in want]
+            job.d_out, job.lse, job.delta = g.data_ptr(), lse.data_ptr(), delta.data_ptr()
+            job.dq, job.dk, job.dv = (t.data_ptr() for t in got)
+            job.ws, job.ws_bytes, job.n_ref = ws.data_ptr(), ws.numel(), plan.n_prefix_tiles
+            extra = (ws, delta, lse, g)
+        vsa.vsa_sync_status(plan)
+        jobs.append(job)
+        checks.append((plan, got, want))
+        keep.append((stream, q, k, v, topk, extra))
+    torch.cuda.synchronize()
+    assert threads(jobs, what) == [(0, b"")] * 2
+    torch.cuda.synchronize()
+    for plan, got, want in checks:
+        vsa.vsa_sync_status(plan)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_first_call_of_a_thread(threads):

@@ -889,8 +889,9 @@ vsa_status launch_bwd_rd(const vsa_plan_s* p, const void* x1, const void* x2, co
   if (!make_map(&m1, x1, rows, D, kBwdM) || !make_map(&m2, x2, rows, D, kBwdM) ||
       !make_map(&m3, y1, rows, D, R) || !make_map(&m4, y2, rows, D, R))
     return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+  // the same leave from every call, so that no other thread's is smaller than this launch
   cudaError_t e = cudaFuncSetAttribute(attn_bwd_kernel<R, D, kKeyMajor>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(kBwdMaxSmem));
   if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
   const int grid = int(std::min<int64_t>(a.n_items, p->num_sms > 0 ? p->num_sms : 148));
   attn_bwd_kernel<R, D, kKeyMajor><<<grid, kThreadsBwd, smem, stream>>>(m1, m2, m3, m4, a);

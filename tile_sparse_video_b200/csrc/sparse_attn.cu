@@ -1499,8 +1499,10 @@ vsa_status launch_rd(const vsa_plan_s* p, const void* q_t, const void* k_t, cons
     return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
   const bool thin = k_ref >= 0;
   auto kernel = thin ? sparse_attn_kernel<R, D, true> : sparse_attn_kernel<R, D, false>;
+  // the same leave from every call: a smaller one, taken by another thread between this and the
+  // launch, would have it refused
   cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
   if (e != cudaSuccess) return fail(VSA_ERR_CUDA, cudaGetErrorString(e));
   AttnArgs a;
   a.topk = topk_idx;
