@@ -296,6 +296,34 @@ def test_destroyed_during_a_capture():
     assert torch.equal(got, want)
 
 
+def test_tables_are_there_when_a_handle_is_returned():
+    """A plan and a rope made while the default stream has work, and used at once on another stream:
+    their tables neither come late nor wait for that work."""
+    args = (9, 70), (4, 24, 24), (4, 4, 4)
+    plan = vsa.Plan(*args)
+    rope = vsa.Rope(plan, (24, 20, 20))
+    xs = randn(1, 1, 2, plan.n_tokens, 64)
+    want, = vsa.vsa_norm_rope(plan, [vsa.HeadTensor(xs)], rope)
+    (tiles, means), = vsa.vsa_norm_rope_permute_pool(plan, [vsa.HeadTensor(xs)], rope)
+    s = torch.cuda.Stream()
+    y, t, m = torch.empty_like(want), torch.empty_like(tiles), torch.empty_like(means)
+    torch.cuda.synchronize()
+    keep = []                                                    # a handle's end waits for the GPU
+    for _ in range(5):
+        torch.cuda._sleep(200_000_000)                           # some 0.1 s
+        new = vsa.Plan(*args)
+        turn = vsa.Rope(new, (24, 20, 20))
+        keep += [new, turn]
+        vsa.vsa_norm_rope(new, [vsa.HeadTensor(xs, y=y)], turn, stream=s)
+        vsa.vsa_norm_rope_permute_pool(new, [vsa.HeadTensor(xs, y=t, pooled=m)], turn, stream=s)
+        s.synchronize()
+        assert not torch.cuda.default_stream().query()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(t, tiles) and torch.equal(m, means)
+        y.zero_(), t.zero_(), m.zero_()
+        vsa.vsa_sync_status(new)
+
+
 def test_repeats_are_bitwise_equal():
     """Sums are taken in a fixed order: two runs give the same bits, the gains' and biases' gradients
     among them, and in split products."""

@@ -273,10 +273,12 @@ vsa_status vsa_rope_create(vsa_plan p, const vsa_rope_desc* desc, vsa_rope* out)
     const size_t nt = r->tab.size() * sizeof(float2), nk = r->tok.size() * sizeof(int4);
     if (e == cudaSuccess) e = cudaMalloc(&r->d_tab, std::max<size_t>(16, nt));
     if (e == cudaSuccess) e = cudaMalloc(&r->d_tok, std::max<size_t>(16, nk));
-    if (e == cudaSuccess && nt > 0)
-      e = cudaMemcpy(r->d_tab, r->tab.data(), nt, cudaMemcpyHostToDevice);
-    if (e == cudaSuccess && nk > 0)
-      e = cudaMemcpy(r->d_tok, r->tok.data(), nk, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) {
+      Upload up;
+      up.copy(r->d_tab, r->tab.data(), nt);
+      up.copy(r->d_tok, r->tok.data(), nk);
+      e = up.finish();
+    }
     if (prev >= 0) cudaSetDevice(prev);
     if (e != cudaSuccess) {
       free_rope(r);

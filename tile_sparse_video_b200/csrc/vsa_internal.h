@@ -71,6 +71,34 @@ class RelaxedCapture {
   cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
 };
 
+// Tables on their way to fresh device memory.  The handle they belong to may be used on any stream
+// as soon as it is returned, so finish() waits for them: cudaMemcpy from pageable memory may return
+// with the copy still to come, and then behind all that the legacy stream has to do.
+class Upload {
+ public:
+  Upload() : error_(cudaStreamCreateWithFlags(&stream_, cudaStreamNonBlocking)) {}
+  ~Upload() {
+    if (stream_ != nullptr) cudaStreamDestroy(stream_);
+  }
+  Upload(const Upload&) = delete;
+  Upload& operator=(const Upload&) = delete;
+  void copy(void* to, const void* from, size_t bytes) {
+    if (error_ == cudaSuccess && bytes > 0)
+      error_ = cudaMemcpyAsync(to, from, bytes, cudaMemcpyHostToDevice, stream_);
+  }
+  void zero(void* to, size_t bytes) {
+    if (error_ == cudaSuccess) error_ = cudaMemsetAsync(to, 0, bytes, stream_);
+  }
+  cudaError_t finish() {
+    if (error_ == cudaSuccess) error_ = cudaStreamSynchronize(stream_);
+    return error_;
+  }
+
+ private:
+  cudaStream_t stream_ = nullptr;
+  cudaError_t error_;
+};
+
 // Kernel launchers (each .cu file); all asynchronous on `stream`.
 cudaError_t launch_gather_rows(const uint16_t* src, uint16_t* dst, const int32_t* map,
                                int64_t bh, int64_t src_rows, int64_t dst_rows, int D,
