@@ -64,7 +64,9 @@ typedef struct vsa_rope_desc {
 /* Builds the rotation of a plan's tokens: angles, cosines and sines in double,
  * kept as fp32 for every distinct position of each axis.  The tables live on
  * the plan's device (host only for a host-only plan), are there for any stream when the call
- * returns, and are owned by the handle, which does not refer to the plan afterwards.  Errors: VSA_ERR_INVALID_ARG
+ * returns, and are owned by the handle, which does not refer to the plan afterwards: it goes with
+ * every plan of the same device, number of prefix tokens and video grid, however these are cut into
+ * segments and tiles, and calls with any other plan refuse it.  Errors: VSA_ERR_INVALID_ARG
  * for dimensions out of range or numbers that are not finite, VSA_ERR_CUDA. */
 vsa_status vsa_rope_create(vsa_plan plan, const vsa_rope_desc* desc, vsa_rope* out);
 

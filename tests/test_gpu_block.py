@@ -253,6 +253,29 @@ def test_norm_rope_refusals():
     vsa.vsa_sync_status(plan)
 
 
+def test_rope_of_another_grid_or_prefix():
+    """As many tokens in another grid, or with more of them in the prefix, stand elsewhere: refused.  Other
+    segments and tiles of the same tokens, and the extents of an empty grid, change no position."""
+    plan = vsa.Plan((9, 7), (2, 4, 6), (4, 4, 4))
+    x = randn(1, 1, 2, plan.n_tokens, 64)
+    want = vsa.vsa_rope_apply(plan, vsa.Rope(plan, (24, 20, 20)), x)
+    others = [vsa.Plan(p, g, (4, 4, 4)) for p, g in (((9, 7), (2, 6, 4)), ((9, 7), (4, 2, 6)), ((40,), (2, 3, 4)))]
+    for other in others:
+        assert other.n_tokens == plan.n_tokens
+        rope = vsa.Rope(other, (24, 20, 20))
+        for call in (lambda: vsa.vsa_rope_apply(plan, rope, x), lambda: vsa.vsa_norm_rope(plan, [vsa.HeadTensor(x)], rope),
+                     lambda: vsa.vsa_norm_rope_permute_pool(plan, [vsa.HeadTensor(x)], rope),
+                     lambda: vsa.vsa_norm_rope_backward(plan, [vsa.HeadGrad(x, x)], rope)):
+            with pytest.raises(vsa.VsaError) as e:
+                call()
+            assert e.value.status == 1
+    for same in (vsa.Plan((16,), (2, 4, 6), (4, 4, 4)), vsa.Plan((1, 15), (2, 4, 6), (4, 8, 4))):
+        assert torch.equal(vsa.vsa_rope_apply(plan, vsa.Rope(same, (24, 20, 20)), x), want)
+    text, none = vsa.Plan((30,), (0, 4, 4), (4, 4, 4)), vsa.Plan((30,), (3, 0, 9), (4, 4, 4))
+    vsa.vsa_rope_apply(text, vsa.Rope(none, (24, 20, 20)), randn(2, 1, 2, 30, 64))
+    vsa.vsa_sync_status(plan)
+
+
 # ---------------------------------------------------------------- linear
 
 # (B, N, x_heads, C, y_heads, O)

@@ -101,10 +101,17 @@ vsa_status check_eps(float eps) {
   return VSA_OK;
 }
 
+// Extent a of a plan's grid, as it tells tokens' positions apart: of an empty grid, none does.
+int extent(const vsa_plan_s* p, int a) { return p->n_tokens > p->n_prefix_tokens ? p->grid[a] : 0; }
+
 vsa_status check_rope(const vsa_plan_s* p, const vsa_rope_s* r, int D) {
   if (r == nullptr) return fail(VSA_ERR_INVALID_ARG, "rope is NULL, and a tensor rotates");
   if (r->device != p->device || r->n_tokens != p->n_tokens)
     return fail(VSA_ERR_INVALID_ARG, "rope was built for another device or number of tokens");
+  // as many tokens in another prefix or grid would turn by the wrong positions
+  bool same = r->n_prefix == p->n_prefix_tokens;
+  for (int a = 0; a < 3; ++a) same = same && r->grid[a] == extent(p, a);
+  if (!same) return fail(VSA_ERR_INVALID_ARG, "rope was built for another prefix length or video grid");
   if (2 * r->P > D) return fail(VSA_ERR_INVALID_ARG, "rope turns more channels than D");
   return VSA_OK;
 }
@@ -179,6 +186,8 @@ vsa_status build_rope(const vsa_plan_s* p, const vsa_rope_desc& d, vsa_rope_s* r
 
   r->device = p->device;
   r->n_tokens = p->n_tokens;
+  r->n_prefix = p->n_prefix_tokens;
+  for (int a = 0; a < 3; ++a) r->grid[a] = extent(p, a);
   r->P = P;
   r->halves = d.halves;
   r->start1 = d.dim[0] / 2;

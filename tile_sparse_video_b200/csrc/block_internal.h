@@ -12,7 +12,8 @@
 // first pair, so that pair p of axis a is tab[tok[n][a] + p].
 struct vsa_rope_s {
   int device = -1;
-  int64_t n_tokens = 0;
+  int64_t n_tokens = 0, n_prefix = 0;
+  int grid[3] = {0, 0, 0};   // the plan's; (0, 0, 0) where it has no video tokens
   int P = 0;                 // rotated pairs
   int start1 = 0, start2 = 0;  // first pair of the height and the width axis
   int halves = 0;
