@@ -164,3 +164,160 @@ def test_planted_mistakes_are_caught(what):
         except AssertionError:
             caught += 1
     assert caught >= 15, (what, caught)
+
+
+class AbortingPair(Pair):
+    """The same with bounded waits, as the kernel gives up: a wait that is over its bound sets its CTA's
+    flag, and each wait of that CTA ends on it; the issuer signals the end of its products, whatever
+    happened.  When all warps of a CTA are through and its flag is set, the leader's producer waits for
+    the copies of its last stages, and the other CTA's gives its own some time.  Time is the scheduler's
+    steps; a copy lands within COPY of them, and a product is done within as many.
+
+    drains: "flag" as above; "own": a producer
+    drains only when its own wait ended early; "never"."""
+    COPY, DRAIN, REST = 150, 1500, 300
+
+    def __init__(self, items, rng, bound, drains="flag"):
+        super().__init__(items, rng)
+        self.bound, self.drains = bound, drains
+        self.now, self.flag, self.drain = 0, [False, False], [Bar(1), Bar(1)]
+        self.live = [10, 10]
+
+    def wait(self, cta, bar, parity, seen):
+        """The generator's value is whether the phase was complete in time."""
+        t0 = self.now
+        while not bar.done(parity, seen):
+            if self.flag[cta] or self.now - t0 > self.bound:
+                self.flag[cta] = True
+                return False
+            yield
+        return True
+
+    def fill(self, cta):
+        """The copies; (K blocks that were asked for, whether that is all of them)."""
+        g = 0
+        for it, n in enumerate(self.items):
+            for kb in range(n):
+                s = g % STAGES
+                if g >= STAGES and not (yield from self.wait(cta, self.empty[cta][s], (g // STAGES - 1) & 1, g // STAGES)):
+                    return g, False
+                if cta == 0:
+                    self.full[s].step(arrivals=1, tx=2 * BYTES)
+                    yield
+
+                def land(s=s, block=(it, kb)):
+                    self.smem[cta][s] = block
+                    self.full[s].step(tx=-BYTES)
+                self.asyncs.append((self.now, land))
+                g += 1
+                yield
+        return g, True
+
+    def producer(self, cta):
+        g, ok = yield from self.fill(cta)
+        while self.live[cta] > 1 and self.drains != "own":
+            yield
+        if self.drains == "never" or (ok if self.drains == "own" else not self.flag[cta]):
+            return
+        t0 = self.now
+        if cta == 0:
+            for x in range(max(0, g - STAGES), g):
+                since = self.now
+                while not self.full[x % STAGES].done((x // STAGES) & 1, x // STAGES + 1) and self.now - since <= self.DRAIN:
+                    yield
+        else:
+            while self.now - t0 < self.REST:
+                yield
+
+    def products(self):
+        g = 0
+        for it, n in enumerate(self.items):
+            buf, use = it % 2, it // 2
+            if use > 0 and not (yield from self.wait(0, self.acc_empty[buf], (use - 1) & 1, use)):
+                return
+            for kb in range(n):
+                s = g % STAGES
+                if not (yield from self.wait(0, self.full[s], (g // STAGES) & 1, g // STAGES + 1)):
+                    return
+                for cta in range(2):
+                    assert self.smem[cta][s] == (it, kb), "the products read another K block"
+
+                def product(s=s):
+                    for cta in range(2):
+                        self.empty[cta][s].step(arrivals=1)
+                self.tensor.append((self.now, product))
+                g += 1
+                yield
+
+            def whole(buf=buf):
+                for cta in range(2):
+                    self.acc_full[cta][buf].step(arrivals=1)
+            self.tensor.append((self.now, whole))
+            yield
+
+    def issuer(self, cta):
+        if cta == 0:
+            yield from self.products()
+            self.tensor.append((self.now, lambda: [b.step(arrivals=1) for b in self.drain]))
+            yield
+        t0 = self.now
+        while not self.drain[cta].done(0, 1) and self.now - t0 <= 100 * self.DRAIN:
+            yield
+
+    def epilogue(self, cta, warp):
+        for it in range(len(self.items)):
+            buf, use = it % 2, it // 2
+            if not (yield from self.wait(cta, self.acc_full[cta][buf], use & 1, use + 1)):
+                return
+            yield
+            self.acc_empty[buf].step(arrivals=1)
+            self.read.append((cta, warp, it))
+            yield
+
+    def run(self, limit=400000):
+        actors = [(c, a) for c in range(2) for a in (self.producer(c), self.issuer(c), *(self.epilogue(c, w) for w in range(8)))]
+        for self.now in range(limit):
+            late = [q for q in (self.asyncs, self.tensor) if q and self.now - q[0][0] > self.COPY]
+            i = self.rng.randrange(len(actors) + 2)
+            if late:
+                late[0].pop(0)[1]()
+            elif i < len(actors):
+                if next(actors[i][1], "end") == "end":
+                    self.live[actors.pop(i)[0]] -= 1
+                    if not actors:                       # both CTAs are at their last barrier
+                        break
+            elif i == len(actors) and self.asyncs:
+                self.asyncs.pop(self.rng.randrange(len(self.asyncs)))[1]()
+            elif i > len(actors) and self.tensor:
+                self.tensor.pop(0)[1]()
+        else:
+            raise AssertionError("the pair did not end")
+        assert not self.asyncs, "a copy is under way when its CTA ends"
+        assert not self.tensor, "a product is under way when its CTA ends"
+        return any(self.flag)
+
+
+def aborts(**how):
+    """Pairs whose waits run out at any point, so that producers stop at different blocks."""
+    for seed in range(200):
+        rng = random.Random(seed)
+        items = [rng.choice([1, 2, 5, 7, 16]) for _ in range(rng.randint(2, 9))]
+        yield AbortingPair(items, rng, rng.choice([5, 20, 60, 100, 150, 250]), **how)
+
+
+def test_pairs_protocol_abort():
+    """The pair ends, with nothing under way."""
+    assert sum(pair.run() for pair in aborts()) >= 100
+
+
+@pytest.mark.parametrize("mistake,said", [(dict(drains="never"), "a copy is"), (dict(drains="own"), "a copy is")],
+                         ids=["no drain", "a drain only for the producer's own waits"])
+def test_planted_mistakes_of_an_abort_are_caught(mistake, said):
+    caught = 0
+    for pair in aborts(**mistake):
+        try:
+            pair.run()
+        except AssertionError as e:
+            assert said in str(e)
+            caught += 1
+    assert caught >= 5, caught

@@ -426,6 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   wait_for_last();
 
+  uint32_t issued = 0;                 // K blocks the producer asked for
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA
     // The whole warp walks the blocks and one lane issues: what the instructions need is then
@@ -498,19 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok) {
-        // abort: none of our TMA writes may still be in flight.  They complete on the leader's
-        // barriers; the other CTA gives its own a millisecond, some thousand times what
-        // a copy takes
-        if (rank == 0) {
-          for (uint32_t x = (g > uint32_t(kStages) ? g - kStages : 0); x < g; ++x)
-            wait_bar_drain(full + 8 * (x % kStages), (x / kStages) & 1);
-        } else {
-          const unsigned long long t0 = globaltimer();
-          while (globaltimer() - t0 < 1000000ull) {
-          }
-        }
-      }
+      issued = g;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -764,6 +753,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (warp == 0 && *abort_flag) {
+    // Abort, whichever warp's: none of our TMA writes may still be in flight.  (Without one all
+    // accumulators came out, and with that all copies in.)  They complete on the leader's
+    // barriers; the other CTA gives its own a millisecond, some thousand times what a copy takes.
+    if (rank == 0) {
+      for (uint32_t x = (issued > uint32_t(kStages) ? issued - kStages : 0); x < issued; ++x)
+        wait_bar_drain(full + 8 * (x % kStages), (x / kStages) & 1);
+    } else {
+      const unsigned long long t0 = globaltimer();
+      while (globaltimer() - t0 < 1000000ull) {
+      }
+    }
+    __syncwarp();
+  }
   cluster_sync();                      // no signal to either CTA is on its way
   if (warp == 1) {
     __syncwarp();
