@@ -173,15 +173,15 @@ class AbortingPair(Pair):
     the copies of its last stages, and the other CTA's gives its own some time.  Time is the scheduler's
     steps; a copy lands within COPY of them, and a product is done within as many.
 
-    drains: "flag" as above; "own": a producer
+    one_deadline: the drain has one bound for all stages.  drains: "flag" as above; "own": a producer
     drains only when its own wait ended early; "never"."""
     COPY, DRAIN, REST = 150, 1500, 300
 
-    def __init__(self, items, rng, bound, drains="flag"):
+    def __init__(self, items, rng, bound, one_deadline=True, drains="flag"):
         super().__init__(items, rng)
-        self.bound, self.drains = bound, drains
+        self.bound, self.one_deadline, self.drains = bound, one_deadline, drains
         self.now, self.flag, self.drain = 0, [False, False], [Bar(1), Bar(1)]
-        self.live = [10, 10]
+        self.live, self.drained = [10, 10], 0
 
     def wait(self, cta, bar, parity, seen):
         """The generator's value is whether the phase was complete in time."""
@@ -222,9 +222,10 @@ class AbortingPair(Pair):
         t0 = self.now
         if cta == 0:
             for x in range(max(0, g - STAGES), g):
-                since = self.now
+                since = t0 if self.one_deadline else self.now
                 while not self.full[x % STAGES].done((x // STAGES) & 1, x // STAGES + 1) and self.now - since <= self.DRAIN:
                     yield
+            self.drained = self.now - t0
         else:
             while self.now - t0 < self.REST:
                 yield
@@ -294,6 +295,8 @@ class AbortingPair(Pair):
             raise AssertionError("the pair did not end")
         assert not self.asyncs, "a copy is under way when its CTA ends"
         assert not self.tensor, "a product is under way when its CTA ends"
+        # a step belongs to one of up to 22 choices, so the last look may come some hundred steps late
+        assert self.drained <= self.DRAIN + 300, "the drain takes more than its bound"
         return any(self.flag)
 
 
@@ -306,12 +309,13 @@ def aborts(**how):
 
 
 def test_pairs_protocol_abort():
-    """The pair ends, with nothing under way."""
+    """The pair ends, with nothing under way, and the drain keeps to its bound."""
     assert sum(pair.run() for pair in aborts()) >= 100
 
 
-@pytest.mark.parametrize("mistake,said", [(dict(drains="never"), "a copy is"), (dict(drains="own"), "a copy is")],
-                         ids=["no drain", "a drain only for the producer's own waits"])
+@pytest.mark.parametrize("mistake,said", [(dict(one_deadline=False), "the drain takes more"), (dict(drains="never"), "a copy is"),
+                                          (dict(drains="own"), "a copy is")],
+                         ids=["a bound for each stage", "no drain", "a drain only for the producer's own waits"])
 def test_planted_mistakes_of_an_abort_are_caught(mistake, said):
     caught = 0
     for pair in aborts(**mistake):

@@ -756,12 +756,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0 && *abort_flag) {
     // Abort, whichever warp's: none of our TMA writes may still be in flight.  (Without one all
     // accumulators came out, and with that all copies in.)  They complete on the leader's
-    // barriers; the other CTA gives its own a millisecond, some thousand times what a copy takes.
+    // barriers, whose phases stay open where the other CTA stopped before them: one bound for all.
+    // The other CTA gives its own a millisecond, some thousand times what a copy takes.
+    const unsigned long long t0 = globaltimer();
     if (rank == 0) {
-      for (uint32_t x = (issued > uint32_t(kStages) ? issued - kStages : 0); x < issued; ++x)
-        wait_bar_drain(full + 8 * (x % kStages), (x / kStages) & 1);
+      uint32_t x = issued > uint32_t(kStages) ? issued - kStages : 0;
+      while (x < issued && globaltimer() - t0 < kWaitLimitNs)
+        if (mbar_try_wait(full + 8 * (x % kStages), (x / kStages) & 1)) ++x;
     } else {
-      const unsigned long long t0 = globaltimer();
       while (globaltimer() - t0 < 1000000ull) {
       }
     }
