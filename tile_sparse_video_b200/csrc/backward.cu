@@ -669,8 +669,9 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       Gs = __shfl_sync(0xFFFFFFFFu, Gs, 0);
       __syncwarp();
     }
-    if (lane == 0 && !ok) {
-      // Abort: let every MMA issued above complete and every TMA copy land.
+    if (lane == 0) {
+      // Every MMA issued above completes and every TMA copy lands before the CTA ends, also where it
+      // is another warp that gives up.
       umma_commit(drain);
       wait_bar_drain(drain, 0);
       for (int s = 0; s < NS; ++s)
@@ -732,8 +733,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(epi_done);
     }
-    if (lane == 0 && !ok) {
-      // Abort: let every MMA this warp issued complete.
+    if (lane == 0) {
+      // every MMA this warp issued completes, also where it is another warp that gives up
       umma_commit(drain2);
       wait_bar_drain(drain2, 0);
     }

@@ -144,11 +144,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
           tma_load_2d(sa + kPABytes, &tm_w, full + 8 * s, kb * kPBK, n * kPBN);
         }
       }
-      if (!ok) {
-        // abort: none of our TMA writes may still be in flight
-        for (uint32_t x = (g > uint32_t(kPStages) ? g - kPStages : 0); x < g; ++x)
-          wait_bar_drain(full + 8 * (x % kPStages), (x / kPStages) & 1);
-      }
+      // none of our TMA writes may still be in flight at the end: with all of them asked for, the
+      // issuer may yet give up before it has waited for them
+      for (uint32_t x = (g > uint32_t(kPStages) ? g - kPStages : 0); x < g; ++x)
+        wait_bar_drain(full + 8 * (x % kPStages), (x / kPStages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {

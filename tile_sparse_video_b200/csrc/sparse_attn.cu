@@ -501,8 +501,9 @@ __device__ __forceinline__ void producer(const AttnArgs& a, const CUtensorMap* t
     __syncwarp();
     if (lane == 0) mbar_arrive(list_empty + 8 * slot);
   }
-  if (lane == 0 && !ok) {
-    // Abort: make sure none of our TMA writes is still in flight.
+  if (lane == 0) {
+    // None of our TMA writes may still be in flight at the end: with all of them asked for, another
+    // warp may yet give up before it has waited for them.
     for (uint32_t x = (g > uint32_t(NS) ? g - NS : 0); x < g; ++x)
       wait_bar_drain(full + 8 * (x % NS), (x / NS) & 1);
     if (kIsK && q_issued > 0) wait_bar_drain(q_full, (q_issued - 1) & 1);
@@ -650,8 +651,9 @@ __device__ __forceinline__ void producer_pair(const AttnArgs& a, const CUtensorM
     __syncwarp();
     if (lane == 0) mbar_arrive(list_empty + 8 * slot);
   }
-  if (lane == 0 && !ok) {
-    // Abort: make sure none of our TMA writes is still in flight.
+  if (lane == 0) {
+    // None of our TMA writes may still be in flight at the end: with all of them asked for, another
+    // warp may yet give up before it has waited for them.
     for (uint32_t x = (g > uint32_t(NS) ? g - NS : 0); x < g; ++x)
       wait_bar_drain(full + 8 * (x % NS), (x / NS) & 1);
     if (kIsK && q_issued > 0) wait_bar_drain(q_full, (q_issued - 1) & 1);
