@@ -119,6 +119,29 @@ def test_host_only_plan_refuses_launches(libvsa):
     rope.close()
 
 
+def test_workspaces_are_looked_at(libvsa):
+    """A workspace that is no tensor, or has gaps, or is on another device than the plan, does not get as
+    far as the library (which refuses the host-only plan itself)."""
+    import torch
+    plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4), device=-1)
+    x, w, y = (torch.zeros(s, dtype=torch.bfloat16) for s in ((1, 4, 64), (64, 64), (1, 4, 64)))
+    h, dw, db = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16), torch.zeros_like(w), torch.zeros(64)
+    for call in (lambda ws: vsa.vsa_linear(plan, x, w, y=y, ws=ws),
+                 lambda ws: vsa.vsa_linear_backward(plan, y, x, w, dx=x, dw=dw, db=db, ws=ws),
+                 lambda ws: vsa.vsa_norm_rope_backward(plan, [vsa.HeadGrad(h, h, None, True, False, h)], ws=ws)):
+        with pytest.raises(TypeError):
+            call(b"0" * 4096)
+        with pytest.raises(ValueError):
+            call(torch.zeros(4096, 2, dtype=torch.uint8)[:, 0])
+    fake = vsa.Plan((4,), (0, 4, 4), (4, 4, 4), device=-1)
+    fake.device = 0                                        # as on a GPU: the workspace is not there
+    for ws in (torch.zeros(4096, dtype=torch.uint8), torch.zeros(4096, 2)[:, 0]):
+        with pytest.raises(ValueError):
+            vsa._workspace(fake, ws)
+    assert vsa._workspace(plan, torch.zeros(3, 5))[1] == 60 and vsa._workspace(plan, None) == (None, 0)
+    plan.close(), fake.close()
+
+
 def test_records_match_the_header(libvsa):
     """The packed records have the sizes and offsets a C compiler gives the header's structures."""
     import subprocess

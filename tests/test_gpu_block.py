@@ -487,6 +487,28 @@ def test_linear_refusals():
     vsa.vsa_sync_status(plan)
 
 
+def test_workspaces_on_the_host_are_refused():
+    """In every call that takes one, the layer's among them: the library sees a pointer and a size only."""
+    plan = vsa.Plan((9,), (2, 4, 4), (4, 4, 4))
+    N = plan.n_tokens
+    x, w, h = randn(1, 1, N, 128), randn(2, 128, 128), randn(3, 1, 2, N, 64)
+    t = vsa.vsa_permute(plan, h)
+    f = torch.zeros(1, 2, plan.n_tiles, 64, device="cuda")
+    rows = torch.zeros(1, 2, plan.n_padded, device="cuda")
+    kept = torch.zeros(1, 2, plan.n_video_tiles, 1, dtype=torch.int32, device="cuda")
+    for ws in (torch.zeros(1 << 22, dtype=torch.uint8), torch.zeros(1 << 22, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        for call in (lambda: vsa.vsa_linear(plan, x, w, ws=ws), lambda: vsa.vsa_linear_backward(plan, x, x, w, ws=ws),
+                     lambda: vsa.vsa_norm_rope_backward(plan, [vsa.HeadGrad(h, h, rotate=False)], ws=ws),
+                     lambda: vsa.vsa_coarse_topk(plan, t, t, t, 1, ws=ws),
+                     lambda: vsa.vsa_coarse_topk_pooled(plan, 1, 2, 64, 1, ws, o_coarse=f, topk_idx=kept),
+                     lambda: vsa.vsa_select_reference(plan, 1, 2, 64, 1, ws, out=kept),
+                     lambda: vsa.vsa_coarse_backward(plan, f, f, f, f, ws),
+                     lambda: vsa.vsa_sparse_attn_backward(plan, t, t, t, t, kept, 1, rows, rows, ws)):
+            with pytest.raises(ValueError):
+                call()
+    vsa.vsa_sync_status(plan)
+
+
 @linears
 def test_linear_backward_dx_add(c):
     """dx_add is added before the one rounding; it may be dx itself; not with x_pre."""

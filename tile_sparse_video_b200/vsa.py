@@ -173,6 +173,19 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _workspace(plan: "Plan", ws: Optional[torch.Tensor]) -> tuple:
+    """(pointer, bytes) of a workspace: a contiguous tensor of any type on the plan's device."""
+    if ws is None:
+        return None, 0
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a torch.Tensor")
+    if ws.get_device() != plan.device:
+        raise ValueError(f"ws must be on the plan's device, cuda:{plan.device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _need(t: torch.Tensor, name: str, dtype, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -290,7 +303,7 @@ def vsa_coarse_topk(plan: Plan, q_t, k_t, v_t, k: int, scale: Optional[float] = 
     _check(lib().vsa_coarse_topk(plan.handle, _ptr(q_t), _ptr(k_t), _ptr(v_t), B, H, D, scale, k,
                                  _ptr(o_coarse), _ptr(topk_idx) if topk_idx.numel() else None,
                                  _ptr(scores) if scores is not None and scores.numel() else None,
-                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+                                 *_workspace(plan, ws), _stream(stream)))
     return o_coarse, topk_idx, scores, ws
 
 
@@ -334,7 +347,7 @@ def vsa_coarse_topk_pooled(plan: Plan, B: int, H: int, D: int, k: int, ws, scale
     _check(lib().vsa_coarse_topk_pooled(plan.handle, B, H, D, scale, k, _ptr(o_coarse),
                                         _ptr(topk_idx) if topk_idx.numel() else None,
                                         _ptr(scores) if scores is not None and scores.numel() else None,
-                                        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+                                        *_workspace(plan, ws), _stream(stream)))
     return o_coarse, topk_idx, scores
 
 
@@ -499,8 +512,7 @@ def vsa_select_reference(plan: Plan, B: int, H: int, D: int, k_ref: int, ws,
     if out is None:
         out = torch.empty(B, H, plan.n_video_tiles, max(k_ref, 0), dtype=torch.int32, device=ws.device)
     _check(lib().vsa_select_reference(plan.handle, B, H, D, scale, k_ref,
-                                      _ptr(out) if out.numel() else None, _ptr(ws),
-                                      ws.numel() * ws.element_size(), _stream(stream)))
+                                      _ptr(out) if out.numel() else None, *_workspace(plan, ws), _stream(stream)))
     return out
 
 
@@ -587,8 +599,7 @@ def vsa_coarse_backward(plan: Plan, qbar, kbar, vbar, d_o_coarse, ws, scale: Opt
         out = tuple(torch.empty_like(qbar) for _ in range(3))
     _check(lib().vsa_coarse_backward(plan.handle, _ptr(qbar), _ptr(kbar), _ptr(vbar),
                                      _ptr(d_o_coarse), B, H, D, scale, _ptr(out[0]), _ptr(out[1]),
-                                     _ptr(out[2]), _ptr(ws), ws.numel() * ws.element_size(),
-                                     _stream(stream)))
+                                     _ptr(out[2]), *_workspace(plan, ws), _stream(stream)))
     return out
 
 
@@ -615,7 +626,7 @@ def vsa_sparse_attn_backward(plan: Plan, q_t, k_t, v_t, d_out_t, topk_idx, k: in
         plan.handle, _ptr(q_t), _ptr(k_t), _ptr(v_t), _ptr(d_out_t),
         _ptr(topk_idx) if topk_idx is not None and topk_idx.numel() else None, k, ref, kr,
         _ptr(lse), _ptr(delta), db[0], db[1], db[2], B, H, D, scale, _ptr(out[0]), _ptr(out[1]),
-        _ptr(out[2]), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        _ptr(out[2]), *_workspace(plan, ws), _stream(stream)))
     return out
 
 
@@ -877,8 +888,7 @@ def vsa_norm_rope_backward(plan: Plan, items: Sequence[HeadGrad], rope: Optional
                  _U8)
     _check(lib().vsa_norm_rope_backward(plan.handle, None if rope is None else rope.handle,
                                         b"".join(records), len(items), eps, bool(tiled), B, H, D,
-                                        ws.data_ptr(), ws.numel() * ws.element_size(),
-                                        _raw_stream(plan, stream)))
+                                        *_workspace(plan, ws), _raw_stream(plan, stream)))
     return res
 
 
@@ -924,9 +934,7 @@ def vsa_linear(plan: Plan, x: torch.Tensor, w: torch.Tensor, bias: Optional[torc
     if ws is None:
         n = _workspace_bytes(plan, "vsa_linear_workspace_size", B, N, C, O)
         ws = _Out(plan, stream)((n,), _U8) if n else None
-    _check(lib().vsa_linear(plan.handle, args, None if ws is None else ws.data_ptr(),
-                            0 if ws is None else ws.numel() * ws.element_size(),
-                            _raw_stream(plan, stream)))
+    _check(lib().vsa_linear(plan.handle, args, *_workspace(plan, ws), _raw_stream(plan, stream)))
     return y
 
 
@@ -963,8 +971,7 @@ def vsa_linear_backward(plan: Plan, dy: torch.Tensor, x: torch.Tensor, w: torch.
                              *_view(plan, dx_add if need[0] else None, "dx_add", x.shape))
     if ws is None:
         ws = out((max(_workspace_bytes(plan, "vsa_linear_backward_workspace_size", B, N, C, O), 16),), _U8)
-    _check(lib().vsa_linear_backward(plan.handle, args, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                     _raw_stream(plan, stream)))
+    _check(lib().vsa_linear_backward(plan.handle, args, *_workspace(plan, ws), _raw_stream(plan, stream)))
     return dx, dw, db
 
 
