@@ -425,6 +425,31 @@ def test_act_backward(act):
     assert torch.equal(vsa.vsa_act_backward(plan, out, pre, act, out=out), got)
 
 
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_slopes_far_out(act):
+    """Where a slope is small it is as exact, relative to itself, as one of the size of 1: 2^t for t = x log2(e)
+    is off by |t| 2^-23 and the rest by some 2^-22, so 2^-18 (1 + |x|) is ample; sigmoid to both sides, SiLU to
+    the left of its slope's root at -1.28, where x (1 - s) and 1 cancel to no less than a quarter."""
+    plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4))
+    pre = torch.cat([torch.linspace(-80, -3, 1024), torch.linspace(3, 80, 1024)]).bfloat16().cuda()
+    if act == "silu":
+        pre = pre[:1024]
+    dy = 1 + torch.arange(pre.numel(), device="cuda").remainder(7).bfloat16()
+    got = f64(vsa.vsa_act_backward(plan, dy, pre, act))
+    # the same through the product of an identity
+    n, w = pre.numel() // 64, torch.eye(64, dtype=torch.bfloat16, device="cuda")
+    rows = [t.view(1, n, 64) for t in (dy, pre)]
+    dx, _, _ = vsa.vsa_linear_backward(plan, rows[0], rows[1], w, x_pre=rows[1], x_act=act, need=(True, False, False))
+    vsa.vsa_sync_status(plan)
+    x, d = f64(pre), f64(dy)
+    e = np.exp(-np.abs(x))
+    want = d * e / (1 + e) ** 2                                  # s(x) s(-x)
+    if act == "silu":
+        want = want * (1 + np.exp(x) + x)                        # s (1 + x s(-x))
+    for g in (got, f64(dx).reshape(-1)):
+        assert np.all(np.abs(g - want) <= (2.0 ** -8 + 2.0 ** -18 * (1 + np.abs(x))) * np.abs(want))
+
+
 def test_linear_strided_and_empty():
     plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4))
     B, N, C, Ow = 2, 70, 128, 192

@@ -267,8 +267,9 @@ __device__ __forceinline__ float2 act_slope2(int act, float2 x) {
     return fma2(mul2(mul2(c, s), fma2(s, both(-1.0f), both(1.0f))), d, s);
   }
   const float2 s = logistic2(mul2(x, both(-kLog2e)));
-  const float2 t = fma2(s, both(-1.0f), both(1.0f));         // 1 - s
-  return act == VSA_ACT_SILU ? fma2(mul2(x, s), t, s) : mul2(s, t);
+  // sigmoid's slope is s(x) s(-x): 1 - s in place of s(-x) loses bits to the right, from x = 17 all of them
+  if (act == VSA_ACT_SIGMOID) return mul2(s, logistic2(mul2(x, both(kLog2e))));
+  return fma2(mul2(x, s), fma2(s, both(-1.0f), both(1.0f)), s);      // there x s (1 - s) adds to 1
 }
 // f *= act'(x).
 template <int kN>
