@@ -49,7 +49,7 @@ constexpr int kMnAtom = 64 * kBK * 2;             // one 64-column x 64-row box
 constexpr int kStaging = 8 * 32 * 64;             // each epilogue warp's 32 rows x 64 bytes
 // full[S], empty[S], acc_full[2], acc_empty[2], drain
 constexpr int kNBar = 2 * kStages + 5;
-constexpr size_t kSmem = size_t(kStages) * kStageBytes + kStaging + 8 * 128 * 4 + kNBar * 8 + 8 + 1024;
+constexpr size_t kSmem = size_t(kStages) * kStageBytes + kStaging + 8 * 128 * 4 + kNBar * 8 + 16 + 1024;
 
 enum Order { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
@@ -389,6 +389,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  acc_empty = acc_full + 16, drain = acc_empty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + kNBar * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + kNBar * 8 + 4);
+  // K blocks the producer asked for (a register of all roles for it made the epilogue spill)
+  uint32_t* issued = reinterpret_cast<uint32_t*>(tail + kNBar * 8 + 8);
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0);
   const int rank = int(cluster_rank());
@@ -427,7 +429,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   wait_for_last();
 
-  uint32_t issued = 0;                 // K blocks the producer asked for
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA
     // The whole warp walks the blocks and one lane issues: what the instructions need is then
@@ -500,7 +501,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      issued = g;
+      if (lane == 0) *issued = g;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -761,8 +762,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // The other CTA gives its own a millisecond, some thousand times what a copy takes.
     const unsigned long long t0 = globaltimer();
     if (rank == 0) {
-      uint32_t x = issued > uint32_t(kStages) ? issued - kStages : 0;
-      while (x < issued && globaltimer() - t0 < kWaitLimitNs)
+      const uint32_t end = *issued;
+      uint32_t x = end > uint32_t(kStages) ? end - kStages : 0;
+      while (x < end && globaltimer() - t0 < kWaitLimitNs)
         if (mbar_try_wait(full + 8 * (x % kStages), (x / kStages) & 1)) ++x;
     } else {
       while (globaltimer() - t0 < 1000000ull) {
