@@ -111,9 +111,10 @@ vsa_status vsa_norm_rope(vsa_plan plan, vsa_rope rope, const vsa_head_tensor* te
 
 /* The same fused with vsa_permute_pool (step 1 of the layer): rows are written in
  * tile order (pad rows 0) and pooled receives the fp32 mean of each tile's live rows,
- * taken before the rounding to bf16.  With norm = rotate = 0 a tensor goes
- * through as vsa_permute_pool would take it.  Q, K and V of a layer take one
- * launch; finish with vsa_coarse_topk_pooled.  y must not overlap x. */
+ * taken before the rounding to bf16.  With norm = rotate = 0 the rows are those of
+ * vsa_permute_pool to the bit; the means are summed in another order (equal up to fp32 rounding, so
+ * that a selection made from them may differ where scores tie that closely).  Q, K and V of a
+ * layer take one launch; finish with vsa_coarse_topk_pooled.  y must not overlap x. */
 vsa_status vsa_norm_rope_permute_pool(vsa_plan plan, vsa_rope rope, const vsa_head_tensor* tensors,
                                       int n, float eps, int B, int H, int D, void* stream);
 

@@ -145,6 +145,25 @@ def test_norm_rope_permute_pool(g):
 
 
 @geos
+def test_means_of_what_only_goes_through(g):
+    """Without norm and rotation the rows are vsa_permute_pool's, and the means too but for the order of the
+    sum: two fp32 sums of up to n terms and a product with 1/n, each within n + 1 roundings of the mean
+    magnitude.  A run after another gives the same bits."""
+    plan, _, _, shape, layout = setup(g)
+    x = laid_out(randn(6, *shape, scale=2.0), layout)
+    (y_t, pooled), = vsa.vsa_norm_rope_permute_pool(plan, [vsa.HeadTensor(x, norm=False, rotate=False)])
+    want_t, want = vsa.vsa_permute_pool(plan, x.contiguous())
+    vsa.vsa_sync_status(plan)
+    assert torch.equal(y_t, want_t)
+    p = O.plan(g[1], g[2], g[3])
+    size = O.pool(O.permute(np.abs(f64(x)), p), p)
+    n = plan.tile_rows
+    assert np.all(np.abs(f64(pooled) - f64(want)) <= 2 * (n + 2) * 2.0 ** -24 * size)
+    again = vsa.vsa_norm_rope_permute_pool(plan, [vsa.HeadTensor(x, norm=False, rotate=False)])[0][1]
+    assert torch.equal(pooled, again)
+
+
+@geos
 @pytest.mark.parametrize("tiled", [False, True])
 def test_norm_rope_backward(g, tiled):
     plan, rope, ang, shape, layout = setup(g)

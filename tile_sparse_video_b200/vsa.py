@@ -1013,7 +1013,9 @@ class Layer:
     is read in natural order): 5 launches.  ``fused=False``: the unfused chain
     (permute Q, K, V, G; pool + coarse + top-k; attention; combine).  Buffers
     are allocated once and reused by every call.  ``qk`` (a QKNormRope): Q and K are
-    normed and rotated in the permuting pass, 3 launches in all when fused."""
+    normed and rotated in the permuting pass, 3 launches in all when fused.  The tile means are then
+    summed in another order, and in the fused form before the rows are rounded to bf16: scores that tie
+    that closely may be selected differently."""
 
     def __init__(self, plan: Plan, B: int, H: int, D: int, k: int, scale: Optional[float] = None,
                  device=None, fused: bool = True, k_ref: Optional[int] = None,
