@@ -169,6 +169,15 @@ int main() {
                        vsa.struct.calcsize("@iiiiiqPqqqPqqqPPqqq"), S("iiiiiqPqqqPqqqPPqqqiPqqqPP")]
 
 
+def test_binding_defines_every_name_once():
+    """A second definition would silently take the place of the first."""
+    import ast
+    body = ast.parse(open(vsa.__file__).read()).body
+    names = [n.name for n in body if isinstance(n, (ast.FunctionDef, ast.ClassDef))]
+    names += [t.id for n in body if isinstance(n, ast.Assign) for t in n.targets if isinstance(t, ast.Name)]
+    assert sorted(set(names)) == sorted(names), sorted(n for n in set(names) if names.count(n) > 1)
+
+
 def _diff(f, x, d, h=1e-5):
     return (f(x + h * d) - f(x - h * d)) / (2 * h)
 

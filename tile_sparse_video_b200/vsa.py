@@ -74,21 +74,6 @@ _LINEAR = struct.Struct("@iiiiiqPqqqPPiiPqqqPqqqPqqq")
 _LINEAR_GRAD = struct.Struct("@iiiiiqPqqqPqqqPPqqqiPqqqPPPqqq")
 
 
-class _RopeDesc(ctypes.Structure):
-    _fields_ = [("dim", ctypes.c_int32 * 3), ("halves", ctypes.c_int32), ("theta", ctypes.c_double * 3),
-                ("offset", ctypes.c_double * 3), ("step", ctypes.c_double * 3),
-                ("inv_freq", ctypes.c_void_p), ("prefix_pos", ctypes.c_void_p)]
-
-
-# Records of include/vsa_block.h, packed by the platform's C rules (a ctypes structure of
-# views costs more host time a call than the launch).  A view is "Pqqq".
-_VIEW = struct.Struct("@Pqqq")
-_HEAD_TENSOR = struct.Struct("@PqqqPiiiPqqqP")
-_HEAD_GRAD = struct.Struct("@PqqqPqqqPiiiPqqqP")
-_LINEAR = struct.Struct("@iiiiiqPqqqPPiiPqqqPqqqPqqq")
-_LINEAR_GRAD = struct.Struct("@iiiiiqPqqqPqqqPPqqqiPqqqPPPqqq")
-
-
 def lib():
     """Load libvsa.so (once).  Raises if it has not been built."""
     global _lib
