@@ -583,6 +583,26 @@ def test_permute_pool_without_means():
     vsa.vsa_sync_status(plan)
 
 
+@pytest.mark.parametrize("c", [(33920, 64, 128), (33920, 2048, 2304), (104704, 264, 72)], ids=lambda c: "x".join(map(str, c)))
+def test_weight_gradient_over_many_rows(c):
+    """dw against what its sum may lose, and not against the sum of magnitudes, which over many rows of random
+    sign is far larger than dw.  A step takes 16 rows: their products and the sum so far are aligned to the
+    largest of them and cut to 24 bits or more (17 terms, each less than 2^-23 of the largest), and the result
+    is cut to 24 bits.  In whatever pieces the rows are summed, a sum of neighbouring rows is no larger than the
+    range R of the running sum; joining up to 16 pieces is 16 more such roundings of R.  So (K/16 + 16) steps of
+    18 * 2^-23 of R, or of the largest product."""
+    M, C, Ow = c
+    plan = vsa.Plan((4,), (0, 4, 4), (4, 4, 4))
+    x, dy, w = randn(1, 1, M, C), randn(2, 1, M, Ow), randn(3, Ow, C, scale=0.1)
+    _, dw, _ = vsa.vsa_linear_backward(plan, dy, x, w, need=(False, True, False))
+    vsa.vsa_sync_status(plan)
+    o, i = [0, Ow // 2, Ow - 1], [0, 7, C // 2, C - 1]
+    terms = f64(dy[0][:, o])[:, :, None] * f64(x[0][:, i])[:, None, :]
+    run = np.concatenate([np.zeros((1, len(o), len(i))), np.cumsum(terms, 0)])
+    big = np.maximum(run.max(0) - run.min(0), np.abs(terms).max(0))
+    close(dw[o][:, i], run[-1], (M / 16 + 17) * 18 * 2.0 ** -23 * big, "dw")
+
+
 def test_offsets_past_32_bits_norm_rope():
     """2.25 G elements a tensor, token strides of 21,504: sampled rows at both ends."""
     plan = vsa.Plan((256,), (32, 48, 68), (4, 8, 4))
