@@ -260,15 +260,7 @@ def prepare(case, seed):
         if own:
             from tile_sparse_video_b200 import vsa
             s["plan"] = vsa.Plan((case["B"] * case["N"],), (0, 4, 4), (4, 4, 4))
-            if op == "linear":
-                s["y"] = torch.empty_like(_rows_like(case, s, "y_heads", "O"))
-                s["pre"] = torch.empty_like(s["y"]) if case["pre"] else None
-            elif op == "act_backward":
-                s["out"] = torch.empty_like(s["dy"])
-            else:
-                s["dx"] = torch.empty_like(s["x"])
-                s["dw"] = torch.empty_like(s["w"])
-                s["db"] = torch.empty(case["O"], device=DEV)
+            if op == "linear_backward":
                 s["ws"] = vsa.linear_backward_workspace(s["plan"], case["B"], case["N"], case["C"], case["O"])
         return s
     if own:
@@ -318,13 +310,14 @@ def _run_own(s):
         out = vsa.vsa_norm_rope_backward(plan, items, s["rope"], eps=EPS, tiled=case["tiled"], ws=s["ws"])
         return [t for pair in out for t in pair if t is not None]
     if op == "act_backward":
-        return vsa.vsa_act_backward(plan, s["dy"], s["pre"], case["act"], out=s["out"])
+        return vsa.vsa_act_backward(plan, s["dy"], s["pre"], case["act"])
     if op == "linear":
+        pre = _rows_like(case, s, "y_heads", "O") if case["pre"] else None
         y = vsa.vsa_linear(plan, s["x"], s["w"], bias=s["bias"], act=case["act"], residual=s["residual"],
-                           y=s["y"], pre=s["pre"])
-        return [y, s["pre"]] if case["pre"] else [y]
+                           y_heads=case["y_heads"], pre=pre)
+        return [y, pre] if case["pre"] else [y]
     return list(vsa.vsa_linear_backward(plan, s["dy"], s["x"], s["w"], x_pre=s["x_pre"], x_act=case["act"],
-                                        dx=s["dx"], dw=s["dw"], db=s["db"], ws=s["ws"]))
+                                        ws=s["ws"]))
 
 
 def _act32(x, act):
