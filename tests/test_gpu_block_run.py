@@ -324,6 +324,23 @@ def test_tables_are_there_when_a_handle_is_returned():
         vsa.vsa_sync_status(new)
 
 
+def test_a_failed_call_does_not_fail_the_next():
+    """A call that CUDA refuses (a runner of some terabytes) leaves nothing behind for those after it."""
+    plan = vsa.Plan((9, 70), (4, 24, 24), (4, 4, 4))
+    rope = vsa.Rope(plan, (24, 20, 20))
+    x, w = randn(1, 1, 2, plan.n_tokens, 64), randn(2, 128, 128)
+    calls = [lambda: vsa.vsa_rope_apply(plan, rope, x), lambda: vsa.vsa_linear(plan, x, w),
+             lambda: vsa.vsa_linear(plan, x[:, :, :3], w), lambda: vsa.vsa_permute(plan, x),
+             lambda: vsa.vsa_act_backward(plan, x, x, "silu")]
+    for call in calls:
+        want = call()
+        with pytest.raises(vsa.VsaError) as e:
+            vsa.LayerPipeline(plan, 4096, 4096, 128, 1)
+        assert e.value.status == 5, e.value
+        assert torch.equal(call(), want)
+    vsa.vsa_sync_status(plan)
+
+
 def test_repeats_are_bitwise_equal():
     """Sums are taken in a fixed order: two runs give the same bits, the gains' and biases' gradients
     among them, and in split products."""

@@ -23,6 +23,9 @@ void set_error(const std::string& msg) { g_last_error = msg; }
 
 vsa_status fail(vsa_status code, const std::string& msg) {
   g_last_error = msg;
+  // the runtime keeps a refused call's error until it is asked for, and the next launch would be
+  // taken for the one that failed
+  if (code == VSA_ERR_CUDA) (void)cudaGetLastError();
   return code;
 }
 
