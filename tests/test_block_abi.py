@@ -169,6 +169,29 @@ int main() {
                        vsa.struct.calcsize("@iiiiiqPqqqPqqqPPqqq"), S("iiiiiqPqqqPqqqPPqqqiPqqqPP")]
 
 
+def test_no_memory_is_an_error(libvsa):
+    """A plan and a rope whose tables find no room: an error, and the process goes on."""
+    import subprocess
+    import sys
+    code = """
+import resource
+from tile_sparse_video_b200 import vsa
+small = vsa.Plan((1 << 24,), (0, 4, 4), (4, 4, 4), device=-1)
+used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (used + (1 << 27), resource.RLIM_INFINITY))
+for make in (lambda: vsa.Plan((1 << 29,), (0, 4, 4), (4, 4, 4), device=-1), lambda: vsa.Rope(small, (24, 20, 20))):
+    try:
+        make()
+        print("made")
+    except vsa.VsaError as e:
+        print(e)
+resource.setrlimit(resource.RLIMIT_AS, (resource.RLIM_INFINITY, resource.RLIM_INFINITY))
+print(vsa.Plan((9,), (0, 4, 4), (4, 4, 4), device=-1).n_tokens)
+"""
+    run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert run.stdout.splitlines() == ["VSA_ERR_INVALID_ARG: out of host memory"] * 2 + ["9"], run
+
+
 def test_binding_defines_every_name_once():
     """A second definition would silently take the place of the first."""
     import ast

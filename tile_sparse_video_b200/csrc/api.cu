@@ -3,6 +3,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <exception>
 #include <new>
 #include <string>
 
@@ -84,7 +85,12 @@ vsa_status vsa_plan_create(const vsa_geometry* geom, int device, vsa_plan* out) 
   *out = nullptr;
   vsa_plan_s* p = new (std::nothrow) vsa_plan_s();
   if (p == nullptr) return fail(VSA_ERR_INVALID_ARG, "out of host memory");
-  vsa_status st = build_plan(*geom, p);
+  vsa_status st;
+  try {
+    st = build_plan(*geom, p);
+  } catch (const std::exception&) {          // the tables' memory: nothing is thrown past a C entry
+    st = fail(VSA_ERR_INVALID_ARG, "out of host memory");
+  }
   if (st != VSA_OK) {
     delete p;
     return st;
