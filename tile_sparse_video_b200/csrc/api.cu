@@ -4,6 +4,8 @@
 #include <cmath>
 #include <cstdio>
 #include <exception>
+#include <map>
+#include <mutex>
 #include <new>
 #include <string>
 
@@ -28,6 +30,18 @@ vsa_status fail(vsa_status code, const std::string& msg) {
   // taken for the one that failed
   if (code == VSA_ERR_CUDA) (void)cudaGetLastError();
   return code;
+}
+
+cudaStream_t upload_stream(cudaError_t* error) {
+  static std::mutex mutex;
+  static std::map<int, cudaStream_t> streams;
+  int device = 0;
+  *error = cudaGetDevice(&device);
+  if (*error != cudaSuccess) return nullptr;
+  const std::lock_guard<std::mutex> lock(mutex);
+  cudaStream_t& s = streams[device];
+  if (s == nullptr) *error = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  return s;
 }
 
 static vsa_status cuda_fail(cudaError_t e, const char* what) {

@@ -71,17 +71,16 @@ class RelaxedCapture {
   cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
 };
 
+// A stream of the current device for uploads, which waits for no other; the library's for good (making
+// one takes 100 us, three times a small plan's creation).  NULL with *error set where there is none.
+cudaStream_t upload_stream(cudaError_t* error);
+
 // Tables on their way to fresh device memory.  The handle they belong to may be used on any stream
 // as soon as it is returned, so finish() waits for them: cudaMemcpy from pageable memory may return
 // with the copy still to come, and then behind all that the legacy stream has to do.
 class Upload {
  public:
-  Upload() : error_(cudaStreamCreateWithFlags(&stream_, cudaStreamNonBlocking)) {}
-  ~Upload() {
-    if (stream_ != nullptr) cudaStreamDestroy(stream_);
-  }
-  Upload(const Upload&) = delete;
-  Upload& operator=(const Upload&) = delete;
+  Upload() : stream_(upload_stream(&error_)) {}
   void copy(void* to, const void* from, size_t bytes) {
     if (error_ == cudaSuccess && bytes > 0)
       error_ = cudaMemcpyAsync(to, from, bytes, cudaMemcpyHostToDevice, stream_);
@@ -95,8 +94,8 @@ class Upload {
   }
 
  private:
-  cudaStream_t stream_ = nullptr;
-  cudaError_t error_;
+  cudaError_t error_ = cudaSuccess;
+  cudaStream_t stream_;
 };
 
 // Kernel launchers (each .cu file); all asynchronous on `stream`.
