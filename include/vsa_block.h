@@ -11,7 +11,7 @@
  * The conventions of vsa.h hold for every call (ownership, alignment, streams,
  * errors, NVTX ranges), with one difference: tensors that come with a vsa_view
  * may be strided.  Calls on a plan keep nothing in it but a recorded fault, and
- * may overlap on the GPU (several streams); a workspace and an output belong to one call
+ * may overlap on the GPU (several streams) and come from several host threads; a workspace and an output belong to one call
  * at a time, and calls or captured graphs that may overlap need their own.
  */
 #ifndef VSA_BLOCK_H_

@@ -23,11 +23,12 @@
 // Every wait is bounded (abort flag and status word); the pair meets at cluster
 // barriers before its first and after its last signal.
 //
-// Measured (B200): 33,920 x 5,376 -> 7,168 with bias, GELU and pre-activation out 1.75-2.0 ms = 1,300-1,490
-// TFLOP/s, the library's plain product of the same operands 1.65-1.9 ms in the same runs; gradients 1.75-2.1
-// ms each.  The tensor pipe is active 99 % of the time (ncu) at the 1.1-1.25 GHz to which the 1 kW cap takes the
+// Measured (B200, device time of calls in a row or replayed from a graph): 33,920 x 5,376 -> 7,168 with
+// bias, GELU and pre-activation out 1.77-2.02 ms = 1,295-1,477 TFLOP/s, the library's plain product of the
+// same operands 1.65-1.9 ms in the same runs; both gradients 3.85-4.12 ms = 1,270-1,358.  The tensor pipe is active 99 % of the time (ncu) at the 1.1-1.25 GHz to which the 1 kW cap takes the
 // clock: power bounds it.  2,048 x 5,376 x 5,376: 86 us forward, 77 us weight gradient (library 86-88 and 79).
-// 9,772 x 1,024 -> 1,024 18.8 us (library 18.7), with bias and residual 21.7.  On the way: one lane on the
+// 9,772 x 1,024 -> 1,024 18.8 us (library 18.7), with bias and residual 21.7-22.9 (called through the
+// binding 26.7).  On the way: one lane on the
 // producer's and issuer's loops with divisions in them 1,050-1,250 TFLOP/s, whole warps without
 // divisions 1,400-1,500; branches for every eight values and
 // scalar arithmetic in the epilogue 45 us in place of 34 (4,096 x 1,024 -> 4,096, GELU); cluster-scope
@@ -1160,7 +1161,7 @@ vsa_status launch(const vsa_plan_s* p, const View& av, int a_box, const View& bv
   // Groups of at most 14 column tiles: the 74 tiles in work at a time are then some 5 x 14, and share
   // their rows of A and columns of B in L2.  At 33,920 x 5,376 x 7,168 (28 or 21 column tiles) the weight
   // gradient took 2,040 us with 14, 2,064 with 10 and 2,138 with all 28 (its DRAM reads fall from 8.5 to
-  // 4.5 GB, and with them the power that holds the clock down); the others stay within 2 %.
+  // 5.5 GB, the column sums' 0.4 among them, and with them the power that holds the clock down); the others stay within 2 %.
   const int groups = (a.n_tiles + 13) / 14;
   a.group = (a.n_tiles + groups - 1) / groups;
   a.by_group = make_div(int64_t(a.m_tiles) * a.group);

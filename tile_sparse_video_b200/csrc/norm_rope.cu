@@ -17,11 +17,13 @@
 // neighbours, and 4c .. 4c+3 with P+4c .. P+4c+3 where they are halves (two 8-byte
 // accesses in place of one of 16 bytes, and no exchange between lanes).
 //
-// Measured (B200, device time, share of the measured 6,549 GB/s copy rate): Q, K and V of 104,704
-// tokens x 42 heads into tiles with their means 1,092 us (6.81 GB, 95 %); the rotation alone of 33,920 x 42 on
-// a [B,N,H,D] tensor 114 us (97 %); the backward of Q, K and V there 460 us (97 %); Q and K of 9,772
-// x 8 out of one [B,N,3,H,D] projection 17.1 us (80 MB, 71 %: start and end of so short a kernel);
-// two heads of 366 tokens 4 us (launch).  A warp per tile and head with its loads in registers, which
+// Measured (B200, device time of a pass replayed from a graph, share of the measured 6,549 GB/s copy
+// rate; in brackets called one after another through the binding, inputs changing): Q, K and V of 104,704
+// tokens x 42 heads into tiles with their means 1,091-1,135 us (6.81 GB, 92-95 %; [1,155]); the rotation
+// alone of 33,920 x 42 on a [B,N,H,D] tensor 116 us (96 %; [125]); the backward of Q, K and V there
+// 459-468 us (95-97 %; [497]); Q and K of 9,772 x 8 out of one [B,N,3,H,D] projection 17.8 us (80 MB, 69 %:
+// start and end of so short a kernel; [18.8]); two heads of 366 tokens 2.4 us (launch; [9.9], host time);
+// the backward of three tensors of a ragged batch 6.9 us ([31.5], host time).  A warp per tile and head with its loads in registers, which
 // looked the angles up for every row and head, took 2,031, 252, 815, 39 and 8 us.
 #include <algorithm>
 #include <cmath>
