@@ -4,7 +4,6 @@
 #include <cmath>
 #include <cstdio>
 #include <exception>
-#include <map>
 #include <mutex>
 #include <new>
 #include <string>
@@ -33,10 +32,12 @@ vsa_status fail(vsa_status code, const std::string& msg) {
 }
 
 cudaStream_t upload_stream(cudaError_t* error) {
+  constexpr int kDevices = 256;
   static std::mutex mutex;
-  static std::map<int, cudaStream_t> streams;
+  static cudaStream_t streams[kDevices];
   int device = 0;
   *error = cudaGetDevice(&device);
+  if (*error == cudaSuccess && device >= kDevices) *error = cudaErrorInvalidDevice;
   if (*error != cudaSuccess) return nullptr;
   const std::lock_guard<std::mutex> lock(mutex);
   cudaStream_t& s = streams[device];
